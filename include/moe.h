@@ -111,7 +111,8 @@ typedef enum {
   MOE_W_Q4G64 = 2,
   MOE_W_Q4G32 = 3,   /* as MOE_W_Q4G64 with one scale and bias per 32 elements */
   MOE_W_Q4G128 = 4,  /* ... per 128 elements */
-  MOE_W_Q8G64 = 5    /* 8-bit affine, group 64 */
+  MOE_W_Q8G64 = 5,   /* 8-bit affine, group 64 */
+  MOE_W_F8 = 6       /* e4m3, one fp32 scale per 128 x 128 elements */
 } moe_wfmt;
 
 typedef enum { MOE_REGIME_AUTO = 0, MOE_REGIME_GEMV = 1, MOE_REGIME_TC = 2 } moe_regime;
@@ -142,6 +143,16 @@ typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_GEGLU_TANH = 1 } moe_act;
  *     w_gu uint32 [E][2F][d/4], w_dn uint32 [E][d][F/4], byte j of a word is
  *     element j; s_*, b_* bf16 [E][rows][cols/64]; value = scale * q + bias.
  *     It runs on the weight-streaming SIMT kernels and the tensor cores.
+ *   MOE_W_F8 (8-bit floating point with block scales; no counterpart on the
+ *   source pages, whose quantised experts are affine):
+ *     w_gu e4m3 codes [E][2F][d], w_dn [E][d][F], one byte per element;
+ *     s_gu fp32 [E][2F/128][d/128], s_dn fp32 [E][d/128][F/128], one scale per
+ *     128 x 128 block; value = scale * code. b_* unused (may be NULL). d and F
+ *     are multiples of 128. The activations are multiplied in e4m3 too, with a
+ *     scale per row and 128 elements (moe_quantize_fp8): moe_forward quantises
+ *     x and h itself; the stage calls for these experts are
+ *     moe_grouped_swiglu_fp8 and moe_grouped_down_fp8 (moe_grouped_swiglu and
+ *     moe_grouped_down return MOE_ERR_UNSUPPORTED).
  *   Quantised formats: the scale and bias arrays are 16-byte aligned, like
  *     every other buffer.
  *   act: moe_act, the gate activation of every expert (0, SwiGLU, when the
@@ -289,11 +300,122 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
                        const moe_experts* experts, int T, int k, void* y, void* ws,
                        size_t ws_bytes, moe_regime regime, moe_stream_t stream);
 
+/* ---- 8-bit floating point ------------------------------------------------
+ *
+ * e4m3 codes (sign, 4 exponent and 3 fraction bits, largest value 448, no
+ * infinity) with one fp32 scale per block of 128 elements along K; the value
+ * of a code is scale * code. The source pages have no counterpart. */
+
+/* Quantise rows or weight blocks:
+ *   amax  = max |x| over the finite elements of the group, at least 2^-100
+ *   scale = amax / 448, code = e4m3(x * (448 / amax)), both quotients and the
+ *   product rounded to fp32, the code to nearest even. An element that is not
+ *   finite gets the NaN code and takes no part in amax.
+ *   x     (device) [rows][K], dtype dt; K a multiple of 16
+ *   block 1: a scale per row and 128 columns, s [rows][ceil(K/128)]
+ *         (activations); 128: a scale per 128 x 128 elements,
+ *         s [ceil(rows/128)][ceil(K/128)] (weights; a stack of matrices whose
+ *         row counts are multiples of 128 may be given as one)
+ *   q     (device, out) e4m3 [rows][K]
+ *   s     (device, out) fp32
+ * The last block of a row (or of the rows) may be partial. rows = 0 returns
+ * MOE_OK and launches nothing. */
+moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int block, void* q,
+                            float* s, moe_stream_t stream);
+
+/* Product of two e4m3 operands with block scales (a dense expert, any linear
+ * layer with such weights):
+ *   y[m][n] = sum_kb sa[m][kb] sb[n/128][kb] sum_{k in block kb} a[m][k] b[n][k]
+ *   a  (device) e4m3 [M][K], sa fp32 [M][ceil(K/128)]
+ *   b  (device) e4m3 [N][K], sb fp32 [ceil(N/128)][ceil(K/128)]
+ *   y  (device, out) [M][N], dtype dt; fp32 sums, rounded once. MOE_F16: values
+ *      outside the fp16 range are reported as MOE_ERR_RANGE in the device
+ *      status
+ * K is a multiple of 16; M and N are any sizes. M = 0 returns MOE_OK and
+ * launches nothing. */
+moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int M,
+                          int N, int K, moe_dtype dt, void* y, moe_stream_t stream);
+
+/* moe_grouped_swiglu for MOE_W_F8 experts: gate|up of the sorted rows, the GLU,
+ * and its result quantised in the same launch.
+ *   xq, xs   (device) e4m3 token rows [T][d] and scales [T][d/128], in token
+ *            order (moe_quantize_fp8, block 1); read in place through row_map
+ *   row_map, row_off, tile_off, BM: as for moe_grouped_swiglu
+ *   hq, hs   (device, out) e4m3 [T*k][F] and fp32 [T*k][F/128]:
+ *            h = act(g) * u in fp32, quantised as moe_quantize_fp8 (block 1)
+ *            does it
+ * Regimes: as moe_grouped_swiglu (no fp16 range applies: every scale is fp32). */
+moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_t* row_map,
+                                  const int32_t* row_off, const int32_t* tile_off, int BM, int T,
+                                  int k, const moe_experts* experts, void* hq, float* hs,
+                                  moe_regime regime, moe_stream_t stream);
+
+/* moe_grouped_down for MOE_W_F8 experts.
+ *   hq, hs   (device) as moe_grouped_swiglu_fp8 writes them
+ *   ys       (device, out) [T*k][d] fp16, as moe_grouped_down stores it for
+ *            16-bit activations (moe_combine reads it) */
+moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* row_off,
+                                const int32_t* tile_off, int BM, int T, int k,
+                                const moe_experts* experts, void* ys, moe_regime regime,
+                                moe_stream_t stream);
+
+/* ---- router training ----------------------------------------------------- */
+
+/* The router's balance loss and the per-expert statistics it is made of (no
+ * counterpart on the source pages, which cover the forward pass only). For
+ * each sequence b of n_b valid tokens, p_t = softmax(logits[t]):
+ *   counts[b][e] = slots (t, j) of its valid tokens with topk_idx[t][j] == e
+ *   probs[b][e]  = 1/n_b sum_t p_t[e]
+ *   loss = coef/n_seq sum_b E/(k n_b) sum_e counts[b][e] probs[b][e]
+ * so a uniform router has loss = coef. A sequence without valid tokens has
+ * zeros and adds nothing (it still counts in n_seq).
+ *   logits   (device) fp32 [T][E], as moe_route writes them
+ *   topk_idx (device) int32 [T][k]; ids outside [0, E) are not counted (slots
+ *            that were dropped)
+ *   mask     (device) uint8 [T], 0: the token takes no part and its logits are
+ *            not read; NULL: every token does
+ *   seq_off  (device) int32 [n_seq+1], ascending in [0, T]: sequence b is the
+ *            tokens seq_off[b] .. seq_off[b+1]-1; tokens outside all of them
+ *            take no part. NULL: one sequence of all T tokens (n_seq = 1)
+ *   n_seq    1 .. 65536
+ *   loss     (device, out) fp32 [1]
+ *   counts   (device, out) int32 [n_seq][E]
+ *   probs    (device, out) fp32 [n_seq][E]
+ *   tokens   (device, out) int32 [n_seq]: n_b
+ *   ws       (device) scratch of moe_balance_loss_workspace(T, E, n_seq) bytes
+ *            (contents on entry do not matter; calls that may overlap on the
+ *            GPU need one each)
+ * Logits of -inf have probability 0; a row of nothing else adds no
+ * probability. fp32 sums in a fixed order: the same inputs give the same bits.
+ * T = 0 is valid and writes zeros. */
+size_t moe_balance_loss_workspace(int T, int E, int n_seq);
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                            const int32_t* seq_off, int T, int E, int k, int n_seq, float coef,
+                            float* loss, int32_t* counts, float* probs, int32_t* tokens, void* ws,
+                            size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of moe_balance_loss with respect to the logits, the counts held
+ * constant:
+ *   dlogits[t][e] = dloss coef/n_seq E/(k n_b^2) p_t[e]
+ *                   (counts[b][e] - sum_e' counts[b][e'] p_t[e'])
+ * and zero for tokens that take no part.
+ *   logits, mask, seq_off, T, E, k, n_seq, coef: as given to moe_balance_loss
+ *   counts, tokens (device): as it wrote them
+ *   dloss    (device) fp32 [1]: the loss's own gradient; NULL: 1
+ *   dlogits  (device, out) fp32 [T][E]
+ * T = 0 returns MOE_OK and launches nothing. */
+moe_status moe_balance_loss_backward(const float* logits, const uint8_t* mask,
+                                     const int32_t* seq_off, int T, int E, int k, int n_seq,
+                                     float coef, const int32_t* counts, const int32_t* tokens,
+                                     const float* dloss, float* dlogits, moe_stream_t stream);
+
 /* Where moe_forward keeps each intermediate inside its workspace (byte
  * offsets), the regime it resolves to for experts of weight format wfmt and
  * the BM it sorts with. moe_forward_workspace(...) is its `total`; 0 when the
  * arguments are invalid. x16 holds 16-bit token rows: fp16, or bf16 as
- * given for bf16 experts with bf16 activations on the tensor cores. With q4
+ * given for bf16 experts with bf16 activations on the tensor cores. With
+ * MOE_W_F8 experts x16 holds the e4m3 codes [T][d] and h those of [T*k][F], each
+ * followed, at the next multiple of 256 bytes, by its fp32 scales. With q4
  * experts the whole-layer call may keep h and x16 with every 8 consecutive
  * elements in the order (0, 4, 1, 5, 2, 6, 3, 7), the K order its kernels
  * dequantise in; the routing and sort tables have the layouts moe_route and
@@ -349,8 +471,9 @@ moe_status moe_selftest_wait_timeout(int which, long long cycles, void* scratch,
  * weight and separate gate/up weights; here separate weights are packed once,
  * at load time, rather than streamed as two tensors in every kernel.
  *   fmt            moe_wfmt of all six tensors
- *   w_g, w_u       (device) [E][F][d] (f32/bf16) or uint32 [E][F][d/8] (q4)
- *   s_g, b_g, s_u, b_u (device) q4 only: bf16 [E][F][d/64]; else ignored
+ *   w_g, w_u       (device) [E][F][d] (f32/bf16/e4m3) or uint32 [E][F][d/8] (q4)
+ *   s_g, b_g, s_u, b_u (device) q4: bf16 [E][F][d/64]; e4m3: s_* fp32
+ *                  [E][F/128][d/128], b_* ignored; else ignored
  *   w_gu, s_gu, b_gu   (device, out) the fused tensors, [E][2F][...]
  * One strided device-to-device copy per tensor on `stream`; nothing is
  * allocated. d and F are multiples of 64; E, d, F > 0; the outputs must not

@@ -34,6 +34,8 @@ Storage layouts (all row-major, the library's canonical format):
   ``w_dn`` uint32 [E, d, F/8], ``s_dn``/``b_dn`` bf16 [E, d, F/64];
   element j of a 32-bit word sits in bits [4j, 4j+3] (low nibble first),
   group g covers input elements [64g, 64g+63].
+* f8 experts: ``w_gu`` uint8 (e4m3 codes) [E, 2F, d], ``s_gu`` fp32
+  [E, 2F/128, d/128], ``w_dn`` [E, d, F], ``s_dn`` [E, d/128, F/128]; no biases.
 """
 from __future__ import annotations
 
@@ -58,7 +60,7 @@ class Workload:
     k: int
     F: int
     act: str          # "f32" | "bf16" | "f16"
-    wfmt: str         # "f32" | "bf16" | "q4" (group 64) | "q4g32" | "q4g128" | "q8"
+    wfmt: str         # "f32" | "bf16" | "q4" (group 64) | "q4g32" | "q4g128" | "q8" | "f8"
     bias: str = "none"  # "none" | "normal0.5" | "zipf1.1"
     note: str = ""
 
@@ -149,6 +151,18 @@ def quantize_q8g64(w: torch.Tensor):
     return words.view(torch.uint32), scale, bias
 
 
+def quantize_f8b128(w: torch.Tensor):
+    """Encode fp32 weights [n, K] as e4m3 codes (uint8 [n, K]) with one fp32
+    scale per 128 x 128 block: scale = max|w| / 448 of the block, code =
+    e4m3(w / scale), round to nearest even (data generation only)."""
+    n, K = w.shape
+    assert n % 128 == 0 and K % 128 == 0
+    wb = w.float().reshape(n // 128, 128, K // 128, 128)
+    s = wb.abs().amax(dim=(1, 3)).clamp_min(1e-30) / 448.0
+    q = (wb / s[:, None, :, None]).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    return q.view(torch.uint8).reshape(n, K), s
+
+
 def pack_nibbles(q: torch.Tensor) -> torch.Tensor:
     """Pack integer codes q[..., K] (values 0..15) into uint32 [..., K/8],
     low nibble first. Used to build hand-made fixtures."""
@@ -229,6 +243,11 @@ def make_experts(wl: Workload, seed: int, device="cpu") -> Experts:
             gu.append(p); sgu.append(s); bgu.append(b)
             p, s, b = quantize_q8g64(wdn)
             dn.append(p); sdn.append(s); bdn.append(b)
+        elif wl.wfmt == "f8":
+            p, s = quantize_f8b128(wgu)
+            gu.append(p); sgu.append(s)
+            p, s = quantize_f8b128(wdn)
+            dn.append(p); sdn.append(s)
         elif q4_group(wl.wfmt):
             p, s, b = quantize_q4g64(wgu, q4_group(wl.wfmt))
             gu.append(p); sgu.append(s); bgu.append(b)

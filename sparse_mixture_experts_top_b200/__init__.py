@@ -29,7 +29,10 @@ EXPORTS = ("moe_route", "moe_topk", "moe_sort_rows_workspace", "moe_sort_rows",
            "moe_grouped_swiglu_workspace", "moe_grouped_swiglu", "moe_grouped_down",
            "moe_combine", "moe_forward_workspace", "moe_pack_gate_up",
            "moe_forward", "moe_forward_layout", "moe_device_status", "moe_status_str",
-           "moe_version", "moe_set_wait_cycles", "moe_selftest_wait_timeout")
+           "moe_version", "moe_set_wait_cycles", "moe_selftest_wait_timeout",
+           "moe_quantize_fp8", "moe_fp8_matmul", "moe_grouped_swiglu_fp8",
+           "moe_grouped_down_fp8", "moe_balance_loss_workspace", "moe_balance_loss",
+           "moe_balance_loss_backward")
 
 
 class MoeError(RuntimeError):
@@ -86,6 +89,19 @@ def _load():
     L.moe_status_str.argtypes = [I]
     L.moe_status_str.restype = ctypes.c_char_p
     L.moe_version.restype = ctypes.c_char_p
+    f32 = ctypes.c_float
+    L.moe_quantize_fp8.argtypes = [P, I, I, I, I, P, P, P]
+    L.moe_fp8_matmul.argtypes = [P, P, P, P, I, I, I, I, P, P]
+    L.moe_grouped_swiglu_fp8.argtypes = [P, P, P, P, P, I, I, I, ctypes.POINTER(Experts), P, P, I,
+                                         P]
+    L.moe_grouped_down_fp8.argtypes = [P, P, P, P, I, I, I, ctypes.POINTER(Experts), P, I, P]
+    L.moe_balance_loss_workspace.argtypes = [I, I, I]
+    L.moe_balance_loss_workspace.restype = S
+    L.moe_balance_loss.argtypes = [P, P, P, P, I, I, I, I, f32, P, P, P, P, P, S, P]
+    L.moe_balance_loss_backward.argtypes = [P, P, P, I, I, I, I, f32, P, P, P, P, P]
+    for name in ("moe_quantize_fp8", "moe_fp8_matmul", "moe_grouped_swiglu_fp8",
+                 "moe_grouped_down_fp8", "moe_balance_loss", "moe_balance_loss_backward"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("moe_route", "moe_topk", "moe_sort_rows", "moe_sort_rows_noalloc",
                  "moe_grouped_swiglu",
                  "moe_grouped_down", "moe_combine", "moe_forward", "moe_forward_layout",
@@ -138,9 +154,9 @@ def _dev(*ts):
             raise ValueError("inputs must be contiguous CUDA tensors")
 
 
-W_Q4G32, W_Q4G128, W_Q8G64 = 3, 4, 5
+W_Q4G32, W_Q4G128, W_Q8G64, W_F8 = 3, 4, 5, 6
 _FMT = {"f32": W_F32, "bf16": W_BF16, "q4": W_Q4G64, "q4g32": W_Q4G32, "q4g128": W_Q4G128,
-        "q8": W_Q8G64}
+        "q8": W_Q8G64, "f8": W_F8}
 ACT_SWIGLU, ACT_GEGLU_TANH = 0, 1
 _ACT = {"swiglu": ACT_SWIGLU, "geglu": ACT_GEGLU_TANH}
 
@@ -266,6 +282,188 @@ def combine(ys, inv_order, topk_w, T, k, dtype=torch.bfloat16, stream=None):
     return y
 
 
+# ------------------------------------------------------------------ 8-bit floating point
+
+F8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+
+
+def _codes(t, what):
+    if t.dtype not in (F8, torch.uint8):
+        raise TypeError(f"{what} must be e4m3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+
+
+def _typed(t, dtype, shape, what):
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _here(t, *others):
+    """The launches go to the current device: every tensor must be on it."""
+    dev = t.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for o in others:
+        if o is not None and o.device != dev:
+            raise ValueError(f"tensors are on {dev} and {o.device}")
+
+
+def quantize_fp8(x, block=1, stream=None):
+    """e4m3 codes (x's shape) and fp32 scales of x [rows, K]: a scale per row and
+    128 columns (block=1: [rows, ceil(K/128)], for activations) or per 128 x 128
+    elements (block=128: [ceil(rows/128), ceil(K/128)], for weights). A stack of
+    weights x [E, rows, K] (rows a multiple of 128 for block=128) gives a stack
+    of scales."""
+    _dev(x)
+    _here(x)
+    *lead, rows, K = x.shape
+    if block not in (1, FP8_BLOCK):
+        raise ValueError(f"block must be 1 or {FP8_BLOCK}, got {block}")
+    if lead and block != 1 and rows % FP8_BLOCK:
+        raise ValueError("a stack of weights needs rows in multiples of 128 (a block of "
+                         "scales may not straddle two of them)")
+    n = x.numel() // K if K else 0
+    q = torch.empty(x.shape, dtype=F8, device=x.device)
+    s = torch.empty(*lead, -(-rows // block), -(-K // FP8_BLOCK), dtype=torch.float32,
+                    device=x.device)
+    _check(lib.moe_quantize_fp8(_ptr(x), _dt(x), n, K, block, _ptr(q), _ptr(s), _stream(stream)),
+           "moe_quantize_fp8")
+    return q, s
+
+
+def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
+    """y [M, N] = a . b^T in `dtype` from e4m3 codes a [M, K], b [N, K] and fp32
+    scales sa [M, ceil(K/128)], sb [ceil(N/128), ceil(K/128)]."""
+    _dev(a, sa, b, sb, out)
+    _here(a, sa, b, sb, out)
+    _codes(a, "a")
+    _codes(b, "b")
+    M, K = a.shape
+    N = b.shape[0]
+    KB = -(-K // FP8_BLOCK)
+    if b.shape[1] != K:
+        raise ValueError(f"a is [{M}, {K}] and b [{N}, {b.shape[1]}]: K differs")
+    _typed(sa, torch.float32, (M, KB), "sa")
+    _typed(sb, torch.float32, (-(-N // FP8_BLOCK), KB), "sb")
+    if out is None:
+        out = torch.empty(M, N, dtype=dtype, device=a.device)
+    else:
+        _typed(out, dtype, (M, N), "out")
+    _check(lib.moe_fp8_matmul(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), M, N, K, _dt_of(dtype),
+                              _ptr(out), _stream(stream)), "moe_fp8_matmul")
+    return out
+
+
+def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUTO, stream=None):
+    """-> (hq e4m3 [T*k, F], hs fp32 [T*k, F/128]): gate|up and GLU of f8 experts
+    from quantised token rows xq [T, d], xs [T, d/128] (quantize_fp8)."""
+    _dev(xq, xs)
+    _here(xq, xs, tables.row_map, experts.w_gu)
+    _codes(xq, "xq")
+    T = xq.shape[0]
+    _typed(xs, torch.float32, (T, experts.d // FP8_BLOCK), "xs")
+    if xq.shape[1] != experts.d:
+        raise ValueError(f"xq is {list(xq.shape)}, the experts' d is {experts.d}")
+    if tables.row_map.numel() != T * k:
+        raise ValueError(f"the tables are of {tables.row_map.numel()} rows, not {T} x {k}")
+    ex = experts_struct(experts)
+    hq = torch.empty(T * k, experts.F, dtype=F8, device=xq.device)
+    hs = torch.empty(T * k, -(-experts.F // FP8_BLOCK), dtype=torch.float32, device=xq.device)
+    _check(lib.moe_grouped_swiglu_fp8(_ptr(xq), _ptr(xs), _ptr(tables.row_map),
+                                      _ptr(tables.row_off), _ptr(tables.tile_off), tables.BM, T, k,
+                                      ctypes.byref(ex), _ptr(hq), _ptr(hs), regime,
+                                      _stream(stream)), "moe_grouped_swiglu_fp8")
+    return hq, hs
+
+
+def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AUTO, stream=None):
+    """-> ys fp16 [T*k, d] from quantised rows hq [T*k, F], hs [T*k, F/128]
+    (grouped_swiglu_fp8)."""
+    _dev(hq, hs)
+    _here(hq, hs, tables.row_off, experts.w_dn)
+    _codes(hq, "hq")
+    if tuple(hq.shape) != (T * k, experts.F):
+        raise ValueError(f"hq is {list(hq.shape)}, not [{T} x {k}, {experts.F}]")
+    _typed(hs, torch.float32, (T * k, experts.F // FP8_BLOCK), "hs")
+    ex = experts_struct(experts)
+    ys = torch.empty(T * k, experts.d, dtype=torch.float16, device=hq.device)
+    _check(lib.moe_grouped_down_fp8(_ptr(hq), _ptr(hs), _ptr(tables.row_off),
+                                    _ptr(tables.tile_off), tables.BM, T, k, ctypes.byref(ex),
+                                    _ptr(ys), regime, _stream(stream)), "moe_grouped_down_fp8")
+    return ys
+
+
+# ------------------------------------------------------------------ router training
+
+@dataclass
+class BalanceStats:
+    loss: torch.Tensor      # fp32 []
+    counts: torch.Tensor    # int32 [sequences, E]
+    probs: torch.Tensor     # fp32 [sequences, E]
+    tokens: torch.Tensor    # int32 [sequences]
+
+
+def _balance_args(logits, mask, seq_off):
+    if logits.dtype != torch.float32 or logits.dim() != 2:
+        raise ValueError(f"logits must be fp32 [T, E], got {logits.dtype} {list(logits.shape)}")
+    T = logits.shape[0]
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or
+                             tuple(mask.shape) != (T,)):
+        raise ValueError(f"mask must be bool or uint8 [{T}], got {mask.dtype} {list(mask.shape)}")
+    if seq_off is not None and (seq_off.dtype != torch.int32 or seq_off.dim() != 1 or
+                                seq_off.numel() < 2):
+        raise ValueError("seq_off must be int32 [sequences + 1]")
+    return T, logits.shape[1], 1 if seq_off is None else seq_off.numel() - 1
+
+
+def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
+                 stream=None) -> BalanceStats:
+    """The router's balance loss with its per-expert counts and mean
+    probabilities, per sequence (seq_off int32 [sequences + 1]; all tokens are
+    one where it is left out), from fp32 logits [T, E] and topk_idx int32 [T, k].
+    mask [T]: tokens that are False take no part. ws: a uint8 tensor of
+    moe_balance_loss_workspace bytes to reuse."""
+    _dev(logits, topk_idx, mask, seq_off)
+    _here(logits, topk_idx, mask, seq_off)
+    T, E, B = _balance_args(logits, mask, seq_off)
+    if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must be int32 [{T}, k], got {topk_idx.dtype} "
+                         f"{list(topk_idx.shape)}")
+    k = topk_idx.shape[1]
+    dev = logits.device
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty(B, E, dtype=torch.int32, device=dev)
+    probs = torch.empty(B, E, dtype=torch.float32, device=dev)
+    tokens = torch.empty(B, dtype=torch.int32, device=dev)
+    if ws is None:
+        ws = torch.empty(lib.moe_balance_loss_workspace(T, E, B), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)     # freed here, still in use there
+    _check(lib.moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(mask), _ptr(seq_off), T, E, k, B,
+                                coef, _ptr(loss), _ptr(counts), _ptr(probs), _ptr(tokens),
+                                _ptr(ws), ws.numel(), _stream(stream)), "moe_balance_loss")
+    return BalanceStats(loss, counts, probs, tokens)
+
+
+def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_off=None,
+                          dloss=None, stream=None):
+    """-> dlogits fp32 [T, E], the gradient of balance_loss(logits, ..., coef, mask,
+    seq_off) times dloss (an fp32 tensor of one value; 1 where it is left out)."""
+    _dev(logits, stats.counts, stats.tokens, mask, seq_off, dloss)
+    _here(logits, stats.counts, stats.tokens, mask, seq_off, dloss)
+    T, E, B = _balance_args(logits, mask, seq_off)
+    _typed(stats.counts, torch.int32, (B, E), "stats.counts")
+    _typed(stats.tokens, torch.int32, (B,), "stats.tokens")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+        raise ValueError("dloss must be one fp32 value")
+    d = torch.empty_like(logits)
+    _check(lib.moe_balance_loss_backward(_ptr(logits), _ptr(mask), _ptr(seq_off), T, E, k, B, coef,
+                                         _ptr(stats.counts), _ptr(stats.tokens), _ptr(dloss),
+                                         _ptr(d), _stream(stream)), "moe_balance_loss_backward")
+    return d
+
+
 # ------------------------------------------------------------------ forward
 
 def _fmt_code(fmt) -> int:
@@ -311,7 +509,8 @@ def forward(x, w_router, router_bias, experts, k, regime=REGIME_AUTO, ws=None, o
 
 def pack_gate_up(fmt, w_g, w_u, s_g=None, b_g=None, s_u=None, b_u=None, stream=None):
     """Fused [gate|up] tensors (w_gu, s_gu, b_gu) from separate gate and up
-    projections [E][F][...] on the device; s_gu, b_gu are None unless q4."""
+    projections [E][F][...] on the device; s_gu, b_gu are None unless q4 or q8
+    (f8 has s_gu alone)."""
     _dev(w_g, w_u, s_g, b_g, s_u, b_u)
     E, F = w_g.shape[0], w_g.shape[1]
     fmt_c = _FMT[fmt] if isinstance(fmt, str) else int(fmt)
@@ -323,6 +522,9 @@ def pack_gate_up(fmt, w_g, w_u, s_g=None, b_g=None, s_u=None, b_u=None, stream=N
     if group:
         s_gu = torch.empty((E, 2 * F, d // group), dtype=s_g.dtype, device=s_g.device)
         b_gu = torch.empty_like(s_gu)
+    elif fmt_c == W_F8:
+        s_gu = torch.empty((E, 2 * s_g.shape[1], s_g.shape[2]), dtype=s_g.dtype,
+                           device=s_g.device)
     _check(lib.moe_pack_gate_up(fmt_c, E, d, F, _ptr(w_g), _ptr(s_g), _ptr(b_g), _ptr(w_u),
                                 _ptr(s_u), _ptr(b_u), _ptr(w_gu), _ptr(s_gu), _ptr(b_gu),
                                 _stream(stream)), "moe_pack_gate_up")

@@ -81,6 +81,12 @@ static moe_status check_experts(const moe_experts* ex, int dt) {
           !aligned16(ex->b_dn))
         return MOE_ERR_INVALID_ARG;
       break;
+    case MOE_W_F8:
+      if (dt == MOE_F32) return MOE_ERR_UNSUPPORTED;
+      if (!ex->s_gu || !ex->s_dn) return MOE_ERR_INVALID_ARG;
+      if (!aligned16(ex->s_gu) || !aligned16(ex->s_dn)) return MOE_ERR_INVALID_ARG;
+      if (ex->d % 128 || ex->F % 128) return MOE_ERR_UNSUPPORTED;
+      break;
     default:
       return MOE_ERR_INVALID_ARG;
   }
@@ -111,6 +117,38 @@ static int resolve_regime(int regime, long long R, int E, int dt, int d, int F, 
 static int block_m_for(int regime, long long R, int E) {
   if (regime == MOE_REGIME_TC) return tc_block_m();
   return (R <= 8LL * E) ? 16 : 32;
+}
+
+// Sizes of e4m3 codes of `rows` rows of K and where their scales (one per 128)
+// follow, in a region of fp8_bytes(rows, K).
+static size_t fp8_scales_at(long long rows, int K) { return up256((size_t)rows * K); }
+static size_t fp8_bytes(long long rows, int K) {
+  return fp8_scales_at(rows, K) + (size_t)rows * ((K + 127) / 128) * 4;
+}
+
+// Checks shared by the grouped fp8 calls.
+static moe_status check_fp8_stage(const moe_experts* ex, int BM, int T, int k, int regime) {
+  moe_status st = check_experts(ex, MOE_BF16);
+  if (st != MOE_OK) return st;
+  if (ex->fmt != MOE_W_F8) return MOE_ERR_UNSUPPORTED;
+  st = check_dims(T, ex->d, ex->E, k);
+  if (st != MOE_OK) return st;
+  if (BM < 1) return MOE_ERR_INVALID_ARG;
+  if (regime != MOE_REGIME_AUTO && regime != MOE_REGIME_GEMV && regime != MOE_REGIME_TC)
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+static cudaError_t swiglu_fp8(const void* xq, const float* xs, const uint32_t* rmap,
+                              const int32_t* roff, const int32_t* toff, int BM, int R,
+                              const moe_experts& ex, void* hq, float* hs, cudaStream_t s) {
+  return launch_swiglu_fp8_stream(xq, xs, rmap, roff, toff, BM, R, ex, hq, hs, s);
+}
+
+static cudaError_t down_fp8(const void* hq, const float* hs, const int32_t* roff,
+                            const int32_t* toff, int BM, int R, const moe_experts& ex, void* ys,
+                            int* stp, cudaStream_t s) {
+  return launch_down_fp8_stream(hq, hs, roff, toff, BM, R, ex, ys, stp, s);
 }
 
 // gate|up in the weight-streaming regime: the q4 tensor-core GEMV when it
@@ -265,6 +303,7 @@ moe_status moe_grouped_swiglu(const void* x, moe_dtype dt, const uint32_t* row_m
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
   moe_status st = check_experts(experts, dt);
   if (st != MOE_OK) return st;
+  if (experts->fmt == MOE_W_F8) return MOE_ERR_UNSUPPORTED;   // moe_grouped_swiglu_fp8
   st = check_dims(T, experts->d, experts->E, k);
   if (st != MOE_OK) return st;
   if (BM < 1) return MOE_ERR_INVALID_ARG;
@@ -298,6 +337,7 @@ moe_status moe_grouped_down(const void* h, moe_dtype dt, const int32_t* row_off,
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
   moe_status st = check_experts(experts, dt);
   if (st != MOE_OK) return st;
+  if (experts->fmt == MOE_W_F8) return MOE_ERR_UNSUPPORTED;   // moe_grouped_down_fp8
   st = check_dims(T, experts->d, experts->E, k);
   if (st != MOE_OK) return st;
   if (BM < 1) return MOE_ERR_INVALID_ARG;
@@ -315,6 +355,102 @@ moe_status moe_grouped_down(const void* h, moe_dtype dt, const int32_t* row_off,
     return launched(launch_down_tc(h, row_off, tile_off, (int)R, *experts, ys, status_ptr(), s));
   }
   return launched(down_gemv(h, dt, row_off, tile_off, BM, (int)R, *experts, ys, status_ptr(), s));
+}
+
+moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int block, void* q,
+                            float* s, moe_stream_t stream) {
+  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || K <= 0 || (block != 1 && block != 128)) return MOE_ERR_INVALID_ARG;
+  if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !s) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return MOE_ERR_INVALID_ARG;
+  return launched(launch_quantize_fp8(x, dt, rows, K, block, q, s, (cudaStream_t)stream));
+}
+
+moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int M,
+                          int N, int K, moe_dtype dt, void* y, moe_stream_t stream) {
+  if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
+  if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!a || !sa || !b || !sb || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  return launched(launch_fp8_matmul_stream(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
+                                           (cudaStream_t)stream));
+}
+
+moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_t* row_map,
+                                  const int32_t* row_off, const int32_t* tile_off, int BM, int T,
+                                  int k, const moe_experts* experts, void* hq, float* hs,
+                                  moe_regime regime, moe_stream_t stream) {
+  const moe_status st = check_fp8_stage(experts, BM, T, k, regime);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!xq || !xs || !row_map || !row_off || !tile_off || !hq || !hs) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(xs) || !aligned16(hq) || !aligned16(hs))
+    return MOE_ERR_INVALID_ARG;
+  if (regime == MOE_REGIME_TC) return MOE_ERR_UNSUPPORTED;
+  return launched(swiglu_fp8(xq, xs, row_map, row_off, tile_off, BM, T * k, *experts, hq, hs,
+                             (cudaStream_t)stream));
+}
+
+moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* row_off,
+                                const int32_t* tile_off, int BM, int T, int k,
+                                const moe_experts* experts, void* ys, moe_regime regime,
+                                moe_stream_t stream) {
+  const moe_status st = check_fp8_stage(experts, BM, T, k, regime);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!hq || !hs || !row_off || !tile_off || !ys) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(hq) || !aligned16(hs) || !aligned16(ys)) return MOE_ERR_INVALID_ARG;
+  if (regime == MOE_REGIME_TC) return MOE_ERR_UNSUPPORTED;
+  return launched(down_fp8(hq, hs, row_off, tile_off, BM, T * k, *experts, ys, status_ptr(),
+                           (cudaStream_t)stream));
+}
+
+// sequences of one balance loss at most (their partial sums are per sequence)
+static const int kMaxSeqs = 1 << 16;
+
+size_t moe_balance_loss_workspace(int T, int E, int n_seq) {
+  if (T < 0 || E <= 0 || n_seq < 1) return 0;
+  return balance_workspace_bytes(T, E, n_seq);
+}
+
+static moe_status check_balance(const int32_t* seq_off, int T, int E, int k, int n_seq) {
+  const moe_status st = check_dims(T, 64, E, k);
+  if (st != MOE_OK) return st;
+  if (n_seq < 1 || (!seq_off && n_seq != 1)) return MOE_ERR_INVALID_ARG;
+  return n_seq > kMaxSeqs ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                            const int32_t* seq_off, int T, int E, int k, int n_seq, float coef,
+                            float* loss, int32_t* counts, float* probs, int32_t* tokens, void* ws,
+                            size_t ws_bytes, moe_stream_t stream) {
+  const moe_status st = check_balance(seq_off, T, E, k, n_seq);
+  if (st != MOE_OK) return st;
+  if (!loss || !counts || !probs || !tokens) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits)) return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned16(ws) || ws_bytes < moe_balance_loss_workspace(T, E, n_seq))
+    return MOE_ERR_WORKSPACE;
+  return launched(launch_balance_loss(logits, topk_idx, mask, seq_off, T, E, k, n_seq, coef, loss,
+                                      counts, probs, tokens, ws, (cudaStream_t)stream));
+}
+
+moe_status moe_balance_loss_backward(const float* logits, const uint8_t* mask,
+                                     const int32_t* seq_off, int T, int E, int k, int n_seq,
+                                     float coef, const int32_t* counts, const int32_t* tokens,
+                                     const float* dloss, float* dlogits, moe_stream_t stream) {
+  const moe_status st = check_balance(seq_off, T, E, k, n_seq);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!logits || !counts || !tokens || !dlogits) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(dlogits)) return MOE_ERR_INVALID_ARG;
+  return launched(launch_balance_loss_backward(logits, mask, seq_off, T, E, k, n_seq, coef, counts,
+                                               tokens, dloss, dlogits, (cudaStream_t)stream));
 }
 
 moe_status moe_combine(const void* ys, const uint32_t* inv_order, const float* topk_w, int T, int k,
@@ -347,24 +483,36 @@ moe_status moe_pack_gate_up(int fmt, int E, int d, int F, const void* w_g, const
       if (d % wq_group(fmt)) return MOE_ERR_UNSUPPORTED;
       if (!s_g || !b_g || !s_u || !b_u || !s_gu || !b_gu) return MOE_ERR_INVALID_ARG;
       break;
+    case MOE_W_F8:
+      row_bytes = (size_t)d;
+      if (d % 128 || F % 128) return MOE_ERR_UNSUPPORTED;
+      if (!s_g || !s_u || !s_gu) return MOE_ERR_INVALID_ARG;
+      break;
     default: return MOE_ERR_INVALID_ARG;
   }
   cudaStream_t s = (cudaStream_t)stream;
   // expert e's F gate rows go to rows 0..F-1 of its 2F-row block, its F up
   // rows to rows F..2F-1: a 2-D copy of E blocks of F rows each
-  auto pack = [&](const void* g, const void* u, void* out, size_t rb) -> cudaError_t {
-    const size_t blk = (size_t)F * rb;
+  auto pack_blocks = [&](const void* g, const void* u, void* out, size_t blk) -> cudaError_t {
     cudaError_t e = cudaMemcpy2DAsync(out, 2 * blk, g, blk, blk, (size_t)E,
                                       cudaMemcpyDeviceToDevice, s);
     if (e != cudaSuccess) return e;
     return cudaMemcpy2DAsync(static_cast<char*>(out) + blk, 2 * blk, u, blk, blk, (size_t)E,
                              cudaMemcpyDeviceToDevice, s);
   };
+  auto pack = [&](const void* g, const void* u, void* out, size_t rb) -> cudaError_t {
+    return pack_blocks(g, u, out, (size_t)F * rb);
+  };
   cudaError_t e = pack(w_g, w_u, w_gu, row_bytes);
   if (e == cudaSuccess && wq_group(fmt)) {
     const size_t srb = (size_t)(d / wq_group(fmt)) * 2;   // one row's bf16 scales (or biases)
     e = pack(s_g, s_u, s_gu, srb);
     if (e == cudaSuccess) e = pack(b_g, b_u, b_gu, srb);
+  }
+  // e4m3: one expert's scales are F / 128 rows of d / 128 floats
+  if (e == cudaSuccess && fmt == MOE_W_F8) {
+    const size_t blk = (size_t)(F / 128) * (d / 128) * 4;
+    e = pack_blocks(s_g, s_u, s_gu, blk);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -375,7 +523,7 @@ moe_status moe_forward_layout(int T, int d, int E, int k, int F, moe_dtype dt, m
                               moe_regime regime, moe_ws_layout* out) {
   if (!out) return MOE_ERR_INVALID_ARG;
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
-  if (wfmt < MOE_W_F32 || wfmt > MOE_W_Q8G64) return MOE_ERR_INVALID_ARG;
+  if (wfmt < MOE_W_F32 || wfmt > MOE_W_F8) return MOE_ERR_INVALID_ARG;
   moe_status st = check_dims(T, d, E, k);
   if (st != MOE_OK) return st;
   if (F <= 0) return MOE_ERR_INVALID_ARG;
@@ -400,13 +548,15 @@ moe_status moe_forward_layout(int T, int d, int E, int k, int F, moe_dtype dt, m
   L.row_off = take((size_t)(E + 1) * 4);
   L.tile_off = take((size_t)(E + 1) * 4);
   L.sort_ws = take(sort_workspace_bytes((int)R, E));
-  L.h = take((size_t)R * F * a);      // fp16 (16-bit activations) or fp32
+  // fp16 (16-bit activations) or fp32; e4m3 experts: codes and their scales
+  L.h = take(wfmt == MOE_W_F8 ? fp8_bytes(R, F) : (size_t)R * F * a);
   L.ys = take((size_t)R * d * a);     // fp16 (16-bit activations) or fp32
   L.regime = resolve_regime(regime, R, E, dt, d, F, wfmt, decode_fused_ok(T, k, E, d, F, wfmt, dt));
   L.BM = block_m_for(L.regime, R, E);
   // fp16 token rows: x converted (weight-streaming), or permuted (the
   // one-launch path), or gathered in sorted row order (tensor cores)
-  L.x16 = take(dt == MOE_F32 ? 0 : (size_t)(L.regime == MOE_REGIME_TC ? R : T) * d * 2);
+  // (e4m3 experts: the token rows' codes and scales, in token order)
+  L.x16 = take(wfmt == MOE_W_F8 ? fp8_bytes(T, d) : dt == MOE_F32 ? 0 : (size_t)(L.regime == MOE_REGIME_TC ? R : T) * d * 2);
   L.total = off;
   *out = L;
   return MOE_OK;
@@ -476,7 +626,16 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
   if ((e = launch_sort_rows(idx, T, k, E, L.BM, order, inv, rmap, counts, roff, toff, sws, s)) !=
       cudaSuccess)
     return launched(e);
-  if (regime_run == MOE_REGIME_TC) {
+  if (experts->fmt == MOE_W_F8) {
+    float* xs = (float*)((char*)x16 + fp8_scales_at(T, d));
+    float* hs = (float*)((char*)h + fp8_scales_at(R, F));
+    if ((e = launch_quantize_fp8(x, dt, T, d, 1, x16, xs, s)) != cudaSuccess) return launched(e);
+    if ((e = swiglu_fp8(x16, xs, rmap, roff, toff, L.BM, (int)R, *experts, h, hs, s)) !=
+        cudaSuccess)
+      return launched(e);
+    if ((e = down_fp8(h, hs, roff, toff, L.BM, (int)R, *experts, ys, stp, s)) != cudaSuccess)
+      return launched(e);
+  } else if (regime_run == MOE_REGIME_TC) {
     // h stays in the q4 dequant's permuted K order between the two kernels
     if ((e = launch_swiglu_tc(x, dt, T, rmap, roff, toff, (int)R, *experts, h, x16, stp, s,
                               true)) != cudaSuccess)

@@ -102,4 +102,34 @@ cudaError_t launch_decode_fused(const void* x, int dt, const void* w_router, con
 cudaError_t launch_combine(const void* ys, const uint32_t* inv_order, const float* w, int T, int k,
                            int d, int dt, void* y, cudaStream_t s);
 
+// fp32, bf16 or fp16 rows [rows][K] (K a multiple of 16) to e4m3 codes with a
+// scale per 1 x 128 (block 1) or 128 x 128 (block 128) elements.
+cudaError_t launch_quantize_fp8(const void* x, int dt, int rows, int K, int block, void* q,
+                                float* s, cudaStream_t st);
+
+// y = a . b^T of e4m3 operands with block scales, and the same grouped by
+// expert (gate|up with the GLU, quantised again; down, fp16 ys). The weight-
+// streaming kernels take any row count and any BM.
+cudaError_t launch_fp8_matmul_stream(const void* a, const float* sa, const void* b, const float* sb,
+                                     int M, int N, int K, int out_dt, void* y, int* status,
+                                     cudaStream_t s);
+cudaError_t launch_swiglu_fp8_stream(const void* xq, const float* xs, const uint32_t* row_map,
+                                     const int32_t* row_off, const int32_t* tile_off, int BM, int R,
+                                     const moe_experts& ex, void* hq, float* hs, cudaStream_t s);
+cudaError_t launch_down_fp8_stream(const void* hq, const float* hs, const int32_t* row_off,
+                                   const int32_t* tile_off, int BM, int R, const moe_experts& ex,
+                                   void* ys, int* status, cudaStream_t s);
+
+// The router's balance loss (sequences at seq_off, or one of all T tokens),
+// and the gradient of its logits.
+size_t balance_workspace_bytes(int T, int E, int n_seq);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask,
+                                const int32_t* seq_off, int T, int E, int k, int n_seq, float coef,
+                                float* loss, int32_t* counts, float* probs, int32_t* tokens,
+                                void* ws, cudaStream_t s);
+cudaError_t launch_balance_loss_backward(const float* logits, const uint8_t* mask,
+                                         const int32_t* seq_off, int T, int E, int k, int n_seq,
+                                         float coef, const int32_t* counts, const int32_t* tokens,
+                                         const float* dloss, float* dlogits, cudaStream_t s);
+
 }  // namespace moe
