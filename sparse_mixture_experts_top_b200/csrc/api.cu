@@ -139,15 +139,25 @@ static moe_status check_fp8_stage(const moe_experts* ex, int BM, int T, int k, i
   return MOE_OK;
 }
 
-static cudaError_t swiglu_fp8(const void* xq, const float* xs, const uint32_t* rmap,
-                              const int32_t* roff, const int32_t* toff, int BM, int R,
-                              const moe_experts& ex, void* hq, float* hs, cudaStream_t s) {
+// The regime of a grouped fp8 call
+static int resolve_fp8(int regime, long long R, int E) {
+  if (regime != MOE_REGIME_AUTO) return regime;
+  return R <= 64 || R < E ? MOE_REGIME_GEMV : MOE_REGIME_TC;
+}
+
+static cudaError_t swiglu_fp8(int rg, const void* xq, const float* xs, const uint32_t* rmap,
+                              const int32_t* roff, const int32_t* toff, int BM, int T, int R,
+                              const moe_experts& ex, void* hq, float* hs, int* stp,
+                              cudaStream_t s) {
+  if (rg == MOE_REGIME_TC)
+    return launch_swiglu_fp8_tc(xq, xs, T, rmap, roff, toff, R, ex, hq, hs, stp, s);
   return launch_swiglu_fp8_stream(xq, xs, rmap, roff, toff, BM, R, ex, hq, hs, s);
 }
 
-static cudaError_t down_fp8(const void* hq, const float* hs, const int32_t* roff,
+static cudaError_t down_fp8(int rg, const void* hq, const float* hs, const int32_t* roff,
                             const int32_t* toff, int BM, int R, const moe_experts& ex, void* ys,
                             int* stp, cudaStream_t s) {
+  if (rg == MOE_REGIME_TC) return launch_down_fp8_tc(hq, hs, roff, toff, R, ex, ys, stp, s);
   return launch_down_fp8_stream(hq, hs, roff, toff, BM, R, ex, ys, stp, s);
 }
 
@@ -377,6 +387,9 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
   if (!a || !sa || !b || !sb || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
     return MOE_ERR_INVALID_ARG;
+  if (M > 8)
+    return launched(launch_fp8_matmul_tc(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
+                                         (cudaStream_t)stream));
   return launched(launch_fp8_matmul_stream(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
                                            (cudaStream_t)stream));
 }
@@ -391,9 +404,11 @@ moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_
   if (!xq || !xs || !row_map || !row_off || !tile_off || !hq || !hs) return MOE_ERR_INVALID_ARG;
   if (!aligned16(xq) || !aligned16(xs) || !aligned16(hq) || !aligned16(hs))
     return MOE_ERR_INVALID_ARG;
-  if (regime == MOE_REGIME_TC) return MOE_ERR_UNSUPPORTED;
-  return launched(swiglu_fp8(xq, xs, row_map, row_off, tile_off, BM, T * k, *experts, hq, hs,
-                             (cudaStream_t)stream));
+  int rg = resolve_fp8(regime, (long long)T * k, experts->E);
+  if (regime == MOE_REGIME_AUTO && BM != tc_block_m()) rg = MOE_REGIME_GEMV;
+  if (rg == MOE_REGIME_TC && BM != tc_block_m()) return MOE_ERR_INVALID_ARG;
+  return launched(swiglu_fp8(rg, xq, xs, row_map, row_off, tile_off, BM, T, T * k, *experts, hq,
+                             hs, status_ptr(), (cudaStream_t)stream));
 }
 
 moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* row_off,
@@ -405,8 +420,10 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
   if (T == 0) return MOE_OK;
   if (!hq || !hs || !row_off || !tile_off || !ys) return MOE_ERR_INVALID_ARG;
   if (!aligned16(hq) || !aligned16(hs) || !aligned16(ys)) return MOE_ERR_INVALID_ARG;
-  if (regime == MOE_REGIME_TC) return MOE_ERR_UNSUPPORTED;
-  return launched(down_fp8(hq, hs, row_off, tile_off, BM, T * k, *experts, ys, status_ptr(),
+  int rg = resolve_fp8(regime, (long long)T * k, experts->E);
+  if (regime == MOE_REGIME_AUTO && BM != tc_block_m()) rg = MOE_REGIME_GEMV;
+  if (rg == MOE_REGIME_TC && BM != tc_block_m()) return MOE_ERR_INVALID_ARG;
+  return launched(down_fp8(rg, hq, hs, row_off, tile_off, BM, T * k, *experts, ys, status_ptr(),
                            (cudaStream_t)stream));
 }
 
@@ -551,7 +568,7 @@ moe_status moe_forward_layout(int T, int d, int E, int k, int F, moe_dtype dt, m
   // fp16 (16-bit activations) or fp32; e4m3 experts: codes and their scales
   L.h = take(wfmt == MOE_W_F8 ? fp8_bytes(R, F) : (size_t)R * F * a);
   L.ys = take((size_t)R * d * a);     // fp16 (16-bit activations) or fp32
-  L.regime = resolve_regime(regime, R, E, dt, d, F, wfmt, decode_fused_ok(T, k, E, d, F, wfmt, dt));
+  L.regime = wfmt == MOE_W_F8 ? resolve_fp8(regime, R, E) : resolve_regime(regime, R, E, dt, d, F, wfmt, decode_fused_ok(T, k, E, d, F, wfmt, dt));
   L.BM = block_m_for(L.regime, R, E);
   // fp16 token rows: x converted (weight-streaming), or permuted (the
   // one-launch path), or gathered in sorted row order (tensor cores)
@@ -589,7 +606,7 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
   // AUTO resolves to TC only for shapes and formats the tensor-core kernels
   // tile; an explicit TC request for others is refused
   const int regime_run = L.regime;
-  if (regime_run == MOE_REGIME_TC && !tc_shape_supported(d, F, experts->fmt, dt))
+  if (regime_run == MOE_REGIME_TC && experts->fmt != MOE_W_F8 && !tc_shape_supported(d, F, experts->fmt, dt))
     return MOE_ERR_UNSUPPORTED;
 
   char* base = static_cast<char*>(ws);
@@ -630,10 +647,11 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
     float* xs = (float*)((char*)x16 + fp8_scales_at(T, d));
     float* hs = (float*)((char*)h + fp8_scales_at(R, F));
     if ((e = launch_quantize_fp8(x, dt, T, d, 1, x16, xs, s)) != cudaSuccess) return launched(e);
-    if ((e = swiglu_fp8(x16, xs, rmap, roff, toff, L.BM, (int)R, *experts, h, hs, s)) !=
+    if ((e = swiglu_fp8(regime_run, x16, xs, rmap, roff, toff, L.BM, T, (int)R, *experts, h, hs,
+                        stp, s)) !=
         cudaSuccess)
       return launched(e);
-    if ((e = down_fp8(h, hs, roff, toff, L.BM, (int)R, *experts, ys, stp, s)) != cudaSuccess)
+    if ((e = down_fp8(regime_run, h, hs, roff, toff, L.BM, (int)R, *experts, ys, stp, s)) != cudaSuccess)
       return launched(e);
   } else if (regime_run == MOE_REGIME_TC) {
     // h stays in the q4 dequant's permuted K order between the two kernels

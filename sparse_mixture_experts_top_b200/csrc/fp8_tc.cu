@@ -1,0 +1,597 @@
+// Products of e4m3 rows with e4m3 weights on the tensor cores (tcgen05 / TMEM /
+// TMA): the dense product and the grouped expert products of many rows.
+//
+//   y[m][n] = sum_kb xs[m][kb] ws[n / 128][kb] sum_{k in kb} x[m][k] w[n][k]
+//
+// A unit of work is 128 token rows (the MMA's M, one per TMEM lane) x BN weight
+// rows (its N). One k-block is 128 codes, the block that shares a scale, and
+// also one 128-byte row of a swizzled tile, so a stage of the TMA ring is one
+// k-block. The MMA's accumulator cannot take a factor per row and block, so
+// each k-block's products go to a TMEM buffer of their own, and eight warps
+// read it back, scale it and add it to fp32 registers while the tensor core
+// fills the other buffer. With token rows on the lanes, the factor
+// xs[m][kb] ws[.][kb] is one value per thread and 64 columns: one FMA per element.
+//
+// Warps: 0 loads (TMA: weight boxes of 128 rows; token rows in boxes of 32, or,
+// through row_map, four rows per gather), 1 issues the MMAs, 4..11 scale, add
+// and store: warp w reads TMEM lanes 32 (w % 4) .., and half (w - 4) / 4 of the
+// columns. Register shares: 72 per thread for warps 0..3, 216 for warps 4..11
+// (their sums of up to 128 columns live in registers), 168 at launch.
+//
+// gate|up: the unit's weight rows are 128 gate and the 128 up rows of the same
+// features, so a thread holds both for 64 features; the GLU's result is
+// quantised in the same epilogue, its block's largest magnitude exchanged
+// between the two halves through shared memory.
+//
+// Every mbarrier wait is bounded, as in the other tensor-core kernels.
+#include "fp8.cuh"
+#include "launch.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace fp8tc {
+
+using namespace fp8;
+using namespace tc;
+
+constexpr int BM = 128;                 // token rows per unit (the sort tables' BM)
+constexpr int kMaxE = 1024;
+constexpr int kThreads = 384;
+constexpr int kAccWarp0 = 4;
+constexpr int kAccWarps = 8;
+constexpr int A_BYTES = BM * kBlock;
+constexpr int A_BOX = 32;               // token rows per TMA box
+
+enum { MODE_STORE = 0, MODE_GLU = 1 };
+
+template <int BN> struct Cfg {
+  static constexpr int B_BYTES = BN * kBlock;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int NS = BN == 256 ? 4 : 6;
+  static constexpr int COLS = BN / 2;               // columns per scaling warp
+  static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int BARS = 256;
+  static constexpr int AMAX = 2 * 2 * BM * 4;       // [tile parity][half][row]
+  static constexpr int TABLES = 2 * (kMaxE + 1) * 4;
+  static constexpr int SMEM = 1024 + NS * STAGE + BARS + AMAX + TABLES;
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+struct Params {
+  const float* xs;           // [.][KB] scales of the token rows
+  const uint32_t* row_map;   // GLU: token row of each sorted row
+  const int32_t* row_off;    // null: one dense product of M rows
+  const int32_t* tile_off;
+  int M, E;
+  int N;                     // output columns (GLU: features F)
+  int K, KB;
+  int n_units;               // units per token tile
+  const float* ws;           // [E][scale_rows][KB]
+  int rows_per_group, scale_rows;
+  void* out;
+  float* out_s;              // GLU: [.][N / 128]
+  int out_dt, act;
+  int wide;                  // every output row starts on a 32-byte boundary
+  int* status;
+  long long wait_limit;
+};
+
+// M = 128, N = n, e4m3 x e4m3, fp32 accumulators, both operands K-major
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+// The four MMAs (K-steps of 32 codes) of one k-block into a fresh accumulator;
+// warp-uniform operands, one elected lane issues.
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo,
+                                          uint32_t bhi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred pf, pt, e;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 pf, %5, %5;\n\t"
+      "setp.eq.b32 pt, %5, %5;\n\t"
+      "mov.b64 a0, {%1, %2};\n\tmov.b64 b0, {%3, %4};\n\t"
+      "add.u32 %1, %1, 2;\n\tadd.u32 %3, %3, 2;\n\t"
+      "mov.b64 a1, {%1, %2};\n\tmov.b64 b1, {%3, %4};\n\t"
+      "add.u32 %1, %1, 2;\n\tadd.u32 %3, %3, 2;\n\t"
+      "mov.b64 a2, {%1, %2};\n\tmov.b64 b2, {%3, %4};\n\t"
+      "add.u32 %1, %1, 2;\n\tadd.u32 %3, %3, 2;\n\t"
+      "mov.b64 a3, {%1, %2};\n\tmov.b64 b3, {%3, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a0, b0, %5, pf;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %5, pt;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %5, pt;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %5, pt;\n\t}\n"
+      : "+r"(d), "+r"(alo), "+r"(ahi), "+r"(blo), "+r"(bhi)
+      : "r"(idesc)
+      : "memory");
+}
+
+// four rows of the map's matrix (box 128 x 1) to 512 consecutive bytes
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int x, int r0,
+                                            int r1, int r2, int r3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+
+// 32 columns of this warp's 32 lanes, and the wait for them, in one statement
+// (the registers are written asynchronously until the wait)
+__device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+        "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
+        "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]),
+        "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]),
+        "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
+      : "r"(ta)
+      : "memory");
+}
+
+// 32 bytes to a 32-byte-aligned address: one whole sector per lane
+__device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int R> __device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R> __device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+struct Unit {
+  int e, r0, nv, unit;       // expert, first row, rows, unit within the tile
+};
+
+__device__ __forceinline__ int total_units(const Params& p, const int* s_toff) {
+  return (p.row_off ? s_toff[p.E] : (p.M + BM - 1) / BM) * p.n_units;
+}
+
+__device__ __forceinline__ Unit decode(const Params& p, const int* s_toff, const int* s_roff,
+                                       int u) {
+  Unit r;
+  const int tile = u / p.n_units;
+  r.unit = u - tile * p.n_units;
+  if (!p.row_off) {
+    r.e = 0;
+    r.r0 = tile * BM;
+    r.nv = min(BM, p.M - r.r0);
+    return r;
+  }
+  int lo = 0, hi = p.E - 1;              // the largest e with tile_off[e] <= tile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_toff[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  r.e = lo;
+  r.r0 = s_roff[lo] + (tile - s_toff[lo]) * BM;
+  r.nv = min(BM, s_roff[lo + 1] - r.r0);
+  return r;
+}
+
+// One output row's COLS consecutive columns from column c of N, rounded to out_dt.
+template <int COLS>
+__device__ __forceinline__ void store_row(const Params& p, size_t row, int c, const float (&acc)[COLS],
+                                          bool& over) {
+  const size_t at = row * p.N + c;
+  if (p.out_dt == MOE_F32) {
+    float* o = reinterpret_cast<float*>(p.out) + at;
+    if (p.wide) {
+#pragma unroll
+      for (int j = 0; j < COLS; j += 8) {
+        if (c + j < p.N) {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(acc[j + i]);
+          st32(o + j, v);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < COLS; ++j)
+        if (c + j < p.N) o[j] = acc[j];
+    }
+    return;
+  }
+  const bool f16 = p.out_dt == MOE_F16;
+  uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
+  uint32_t hmax = 0;
+#pragma unroll
+  for (int j = 0; j < COLS; j += 16) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = acc[j + 2 * i], b = acc[j + 2 * i + 1];
+      v[i] = f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+    }
+    if (p.wide) {
+      if (c + j < p.N) st32(o + j, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (c + j + 2 * i < p.N) o[j + 2 * i] = (uint16_t)v[i];
+        if (c + j + 2 * i + 1 < p.N) o[j + 2 * i + 1] = (uint16_t)(v[i] >> 16);
+      }
+    }
+    // columns past N repeat nothing of the product's rows (zero-filled) or are
+    // another expert's: they are not looked at
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c + j + 2 * i < p.N) hmax = max(hmax, v[i] & 0x7FFFu);
+      if (c + j + 2 * i + 1 < p.N) hmax = max(hmax, (v[i] >> 16) & 0x7FFFu);
+    }
+  }
+  over |= f16 && hmax >= 0x7C00u;
+}
+
+template <int MODE, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmA,
+                  const __grid_constant__ CUtensorMap tmB) {
+  using C = Cfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
+  const uint32_t st_base = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);   // [NS]
+  uint64_t* empty = full + C::NS;                                          // [NS]
+  uint64_t* acc_full = empty + C::NS;                                      // [2]
+  uint64_t* acc_empty = acc_full + 2;                                      // [2]
+  uint64_t* xchg = acc_empty + 2;                                          // [1]
+  uint64_t* drain = xchg + 1;                                              // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* s_amax = reinterpret_cast<float*>(smem + C::NS * C::STAGE + C::BARS);
+  int* s_toff = reinterpret_cast<int*>(smem + C::NS * C::STAGE + C::BARS + C::AMAX);
+  int* s_roff = s_toff + kMaxE + 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(empty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(acc_full + i), 1);
+      mbar_init(smem_u32(acc_empty + i), kAccWarps);
+    }
+    mbar_init(smem_u32(xchg), kAccWarps);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "n"(C::TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch();
+  if (p.row_off) {
+    for (int i = threadIdx.x; i <= p.E; i += kThreads) {
+      s_toff[i] = __ldg(p.tile_off + i);
+      s_roff[i] = __ldg(p.row_off + i);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = total_units(p, s_toff);
+
+  if (warp < kAccWarp0) {
+    regs_dec<72>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- loads (TMA)
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const Unit t = decode(p, s_toff, s_roff, u);
+        const int wrow = t.e * p.rows_per_group + t.unit * (MODE == MODE_GLU ? kBlock : BN);
+        // boxes of weight rows that the product has (the rest of the stage
+        // keeps old codes, whose columns are not stored)
+        const int boxes = MODE == MODE_GLU ? 2 : BN < kBlock ? 1
+                          : min(BN, p.N - t.unit * BN) > kBlock ? 2 : 1;
+        constexpr int BOX_BYTES = (BN < kBlock ? BN : kBlock) * kBlock;
+        const int up = MODE == MODE_GLU ? p.N : kBlock;       // second box's row offset
+        int rows[4] = {0, 0, 0, 0};
+        int a_bytes;
+        if (p.row_map) {
+          a_bytes = (t.nv + 3) / 4 * 512;
+          if (4 * lane < t.nv) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              rows[i] = (int)__ldg(p.row_map + t.r0 + min(4 * lane + i, t.nv - 1));
+          }
+        } else {
+          a_bytes = (t.nv + A_BOX - 1) / A_BOX * (A_BOX * kBlock);
+        }
+        for (int kb = 0; kb < p.KB && ok; ++kb, ++it) {
+          const uint32_t s = it % C::NS;
+          if (it >= (uint32_t)C::NS) {
+            ok = mbar_wait_warp(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
+                                true, p.wait_limit);
+            if (!ok) break;
+          }
+          const uint32_t dst = st_base + s * C::STAGE;
+          const uint32_t bar = smem_u32(full + s);
+          const int x = kb * kBlock;
+          if (lane == 0) {
+            mbar_arrive_tx(bar, (uint32_t)(a_bytes + boxes * BOX_BYTES));
+            tma_load_2d(dst + A_BYTES, &tmB, x, wrow, bar);
+            if (boxes == 2) tma_load_2d(dst + A_BYTES + BOX_BYTES, &tmB, x, wrow + up, bar);
+            if (!p.row_map)
+              for (int r = 0; r < t.nv; r += A_BOX)
+                tma_load_2d(dst + r * kBlock, &tmA, x, t.r0 + r, bar);
+          }
+          __syncwarp();
+          if (p.row_map && 4 * lane < t.nv)
+            tma_gather4(dst + lane * 512, &tmA, x, rows[0], rows[1], rows[2], rows[3], bar);
+        }
+      }
+      for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
+        const uint32_t last = it - 1 - i;
+        mbar_wait_warp(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status,
+                       false);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t da = desc_sw128(st_base), db = desc_sw128(st_base + A_BYTES);
+      const uint32_t alo0 = (uint32_t)da, ahi = (uint32_t)(da >> 32);
+      const uint32_t blo0 = (uint32_t)db, bhi = (uint32_t)(db >> 32);
+      constexpr uint32_t kStage16 = C::STAGE >> 4;
+      const uint32_t idesc = idesc_e4m3(BN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        for (int kb = 0; kb < p.KB; ++kb, ++it) {
+          const uint32_t s = it % C::NS, b = it & 1;
+          // buffer b was read back two k-blocks ago
+          if (it >= 2)
+            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it >> 1) - 1) & 1, abort_flag, p.status,
+                                true, p.wait_limit);
+          if (!ok) break;
+          ok = mbar_wait_warp(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
+                              p.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t off = s * kStage16;
+          mma_block(tm + b * BN, alo0 + off, ahi, blo0 + off, bhi, idesc);
+          mma_commit_warp(smem_u32(empty + s));
+          mma_commit_warp(smem_u32(acc_full + b));
+        }
+      }
+      mma_commit_warp(smem_u32(drain));
+      mbar_wait_warp(smem_u32(drain), 0, abort_flag, p.status, false);
+    }
+  } else {
+    // ------------------------------------------------------------ scale, add, store
+    regs_inc<216>();
+    constexpr int COLS = C::COLS;
+    const int q = warp & 3, half = (warp - kAccWarp0) >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    // the thread's columns: two runs of COLS / 2, one of gate and one of up
+    // columns, or one after the other
+    const int c0 = MODE == MODE_GLU ? half * (COLS / 2) : half * COLS;
+    const int c1 = MODE == MODE_GLU ? BN / 2 + c0 : c0 + COLS / 2;
+    uint32_t it = 0, tiles = 0;
+    bool ok = true, over = false;
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++tiles) {
+      const Unit t = decode(p, s_toff, s_roff, u);
+      const bool live = q * 32 < t.nv;            // some of the warp's lanes are rows
+      const int m = q * 32 + lane;
+      int xrow = t.r0 + min(m, t.nv - 1);
+      if (p.row_map) xrow = (int)__ldg(p.row_map + xrow);
+      const float* sa = p.xs + (size_t)xrow * p.KB;
+      const float* wsc = p.ws + (size_t)t.e * p.scale_rows * p.KB;
+      int n0, n1;                                 // scale rows of the two runs
+      if (MODE == MODE_GLU) {
+        n0 = t.unit;
+        n1 = p.N / kBlock + t.unit;
+      } else {
+        // a run past N has no scale of its own and is not stored
+        n0 = min((t.unit * BN + c0) / kBlock, p.scale_rows - 1);
+        n1 = min((t.unit * BN + c1) / kBlock, p.scale_rows - 1);
+      }
+      const float *w0 = wsc + (size_t)n0 * p.KB, *w1 = wsc + (size_t)n1 * p.KB;
+      float acc[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      float a = __ldg(sa), b0 = __ldg(w0), b1 = __ldg(w1);
+      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+        const float f0 = a * b0, f1 = a * b1;
+        if (kb + 1 < p.KB) {                      // the next block's, ahead of the wait
+          a = __ldg(sa + kb + 1);
+          b0 = __ldg(w0 + kb + 1);
+          b1 = __ldg(w1 + kb + 1);
+        }
+        const uint32_t b = it & 1;
+        ok = mbar_wait_warp(smem_u32(acc_full + b), (it >> 1) & 1, abort_flag, p.status, true,
+                            p.wait_limit);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < COLS; j += 32) {
+            constexpr int H = COLS / 2;
+            uint32_t d[32];
+            tmem_ld32(tl + b * BN + (j < H ? c0 + j : c1 + j - H), d);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              acc[j + i] = fmaf(__uint_as_float(d[i]), j < H ? f0 : f1, acc[j + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
+      }
+      if (!ok) break;
+      if (MODE == MODE_STORE) {
+        if (m < t.nv) store_row<COLS>(p, (size_t)t.r0 + m, t.unit * BN + c0, acc, over);
+      } else {
+        constexpr int H = COLS / 2;
+        float mx = 0.f;
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            acc[j] = glu(p.act, acc[j], acc[H + j]);
+            mx = fmaxf(mx, finite_abs(acc[j]));
+          }
+        }
+        // the block's other 64 features are the other half's warp. The arrays
+        // alternate: one is written again only after every warp has passed
+        // the next tile's exchange, and so has read this one
+        float* am = s_amax + (tiles & 1) * 2 * BM;
+        am[half * BM + m] = mx;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(xchg));
+        ok = mbar_wait_warp(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
+        if (!ok) break;
+        if (m < t.nv) {
+          mx = fmaxf(am[m], am[BM + m]);
+          const float r = rscale_of(mx);
+          uint8_t* o = reinterpret_cast<uint8_t*>(p.out) + ((size_t)t.r0 + m) * p.N +
+                       t.unit * kBlock + c0;
+#pragma unroll
+          for (int j = 0; j < H; j += 32) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = e4m3x4(code_arg(acc[j + 4 * i], r), code_arg(acc[j + 4 * i + 1], r),
+                            code_arg(acc[j + 4 * i + 2], r), code_arg(acc[j + 4 * i + 3], r));
+            if (p.wide) {
+              st32(o + j, v);
+            } else {
+              *reinterpret_cast<uint4*>(o + j) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(o + j + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
+          }
+          if (half == 0)
+            p.out_s[((size_t)t.r0 + m) * (p.N / kBlock) + t.unit] = scale_of(mx);
+        }
+      }
+    }
+    if (MODE == MODE_STORE && over) report_status(p.status, MOE_ERR_RANGE);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::TMEM)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+template <int MODE, int BN>
+static cudaError_t run(Params& p, const void* x, long long x_rows, const void* w, long long tiles,
+                       cudaStream_t s) {
+  p.n_units = MODE == MODE_GLU ? p.N / kBlock : (p.N + BN - 1) / BN;
+  p.wait_limit = wait_cycles();
+  const int esize = MODE == MODE_GLU ? 1 : p.out_dt == MOE_F32 ? 4 : 2;
+  p.wide = (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) && ((long long)p.N * esize) % 32 == 0;
+  // rows are addressed by 32-bit coordinates
+  if ((long long)p.E * p.rows_per_group > 0x7fffffffLL) return cudaErrorNotSupported;
+  CUtensorMap ta, tb;
+  const uint32_t wbox = BN < kBlock ? BN : kBlock;
+  if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, p.K, (uint64_t)x_rows, p.K, kBlock,
+                p.row_map ? 1 : A_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.K, (uint64_t)p.E * p.rows_per_group, p.K,
+                kBlock, wbox, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fp8_tc_kernel<MODE, BN>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long units = tiles * p.n_units;
+  if (units > 0x7fffffffLL) return cudaErrorNotSupported;
+  const int grid = units < num_sms() ? (int)units : num_sms();
+  launch_pdl(fp8_tc_kernel<MODE, BN>, (unsigned)grid, kThreads, Cfg<BN>::SMEM, s, p, ta, tb);
+  return cudaGetLastError();
+}
+
+}  // namespace fp8tc
+
+cudaError_t launch_fp8_matmul_tc(const void* a, const float* sa, const void* b, const float* sb,
+                                 int M, int N, int K, int out_dt, void* y, int* status,
+                                 cudaStream_t s) {
+  using namespace fp8tc;
+  Params p{};
+  p.xs = sa;
+  p.M = M;
+  p.E = 1;
+  p.N = N;
+  p.K = K;
+  p.KB = (K + kBlock - 1) / kBlock;
+  p.ws = sb;
+  p.rows_per_group = N;
+  p.scale_rows = (N + kBlock - 1) / kBlock;
+  p.out = y;
+  p.out_dt = out_dt;
+  p.status = status;
+  return run<MODE_STORE, 256>(p, a, M, b, ((long long)M + BM - 1) / BM, s);
+}
+
+cudaError_t launch_swiglu_fp8_tc(const void* xq, const float* xs, int T, const uint32_t* row_map,
+                                 const int32_t* row_off, const int32_t* tile_off, int R,
+                                 const moe_experts& ex, void* hq, float* hs, int* status,
+                                 cudaStream_t s) {
+  using namespace fp8tc;
+  if (R <= 0) return cudaSuccess;
+  Params p{};
+  p.xs = xs;
+  p.row_map = row_map;
+  p.row_off = row_off;
+  p.tile_off = tile_off;
+  p.E = ex.E;
+  p.N = ex.F;
+  p.K = ex.d;
+  p.KB = ex.d / kBlock;
+  p.ws = (const float*)ex.s_gu;
+  p.rows_per_group = 2 * ex.F;
+  p.scale_rows = 2 * ex.F / kBlock;
+  p.out = hq;
+  p.out_s = hs;
+  p.act = ex.act;
+  p.status = status;
+  return run<MODE_GLU, 256>(p, xq, T, ex.w_gu, max_tiles(R, ex.E, BM), s);
+}
+
+cudaError_t launch_down_fp8_tc(const void* hq, const float* hs, const int32_t* row_off,
+                               const int32_t* tile_off, int R, const moe_experts& ex, void* ys,
+                               int* status, cudaStream_t s) {
+  using namespace fp8tc;
+  if (R <= 0) return cudaSuccess;
+  Params p{};
+  p.xs = hs;
+  p.row_off = row_off;
+  p.tile_off = tile_off;
+  p.E = ex.E;
+  p.N = ex.d;
+  p.K = ex.F;
+  p.KB = ex.F / kBlock;
+  p.ws = (const float*)ex.s_dn;
+  p.rows_per_group = ex.d;
+  p.scale_rows = ex.d / kBlock;
+  p.out = ys;
+  p.out_dt = MOE_F16;
+  p.status = status;
+  return run<MODE_STORE, 256>(p, hq, R, ex.w_dn, max_tiles(R, ex.E, BM), s);
+}
+
+}  // namespace moe

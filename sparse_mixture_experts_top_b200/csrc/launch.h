@@ -120,6 +120,18 @@ cudaError_t launch_down_fp8_stream(const void* hq, const float* hs, const int32_
                                    const int32_t* tile_off, int BM, int R, const moe_experts& ex,
                                    void* ys, int* status, cudaStream_t s);
 
+// The same on the tensor cores: BM must equal tc_block_m().
+cudaError_t launch_fp8_matmul_tc(const void* a, const float* sa, const void* b, const float* sb,
+                                 int M, int N, int K, int out_dt, void* y, int* status,
+                                 cudaStream_t s);
+cudaError_t launch_swiglu_fp8_tc(const void* xq, const float* xs, int T, const uint32_t* row_map,
+                                 const int32_t* row_off, const int32_t* tile_off, int R,
+                                 const moe_experts& ex, void* hq, float* hs, int* status,
+                                 cudaStream_t s);
+cudaError_t launch_down_fp8_tc(const void* hq, const float* hs, const int32_t* row_off,
+                               const int32_t* tile_off, int R, const moe_experts& ex, void* ys,
+                               int* status, cudaStream_t s);
+
 // The router's balance loss (sequences at seq_off, or one of all T tokens),
 // and the gradient of its logits.
 size_t balance_workspace_bytes(int T, int E, int n_seq);

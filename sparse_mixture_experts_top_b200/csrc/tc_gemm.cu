@@ -40,14 +40,11 @@
 // Every mbarrier wait is bounded (about a second): on expiry the kernel
 // records MOE_ERR_TIMEOUT in the status word, all roles leave their loops,
 // copies in flight are waited for (bounded), TMEM is freed, and it returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
-
-#include <mutex>
 
 #include "common.cuh"
 #include "launch.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace tc {
@@ -69,7 +66,6 @@ constexpr int kMaxE = 1024;    // tile / row tables cached in shared memory
 constexpr int kThreads = 768;   // 24 warps
 constexpr int kEpiWarp0 = 4;
 constexpr int kDqWarp0 = 8;
-constexpr long long kWaitCycles = 2000000000LL;   // ~1 s at the B200's clocks
 
 // EPI_SWIGLU / EPI_GEGLU: gate|up, h = act(gate) * up in fp16, the gate
 // activation fixed at compile time (a runtime choice in the unrolled
@@ -148,99 +144,6 @@ struct Params {
 
 // ------------------------------------------------------------------ PTX
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// try_wait with a suspend-time hint: a thread whose phase is not complete
-// sleeps until it completes or about `ns` nanoseconds pass, instead of
-// spinning and taking issue slots from the warps that do the work
-__device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait for the phase of `parity` to complete: at most `limit` SM
-// cycles. Returns false when the kernel is aborting (another role timed out;
-// ignored when !honor_abort) or this wait ran out. Waits for work use the
-// launch's bound (Params::wait_limit); the waits for copies and MMAs still in
-// flight before the CTA exits keep the full bound, so that nothing lands in
-// shared memory or TMEM after the CTA has released it. A bound below ~50 us
-// also drops the sleep hint, so the wait notices its deadline promptly.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          int* status, bool honor_abort = true,
-                                          long long limit = kWaitCycles) {
-  if (mbar_try(bar, parity)) return true;
-  const long long t0 = clock64();
-  const bool sleep = limit >= 100000;
-  const uint32_t af = smem_u32(const_cast<const int*>(abort_flag));
-  for (;;) {
-    if (sleep ? mbar_try_sleep(bar, parity, 20000u) : mbar_try(bar, parity)) return true;
-    uint32_t aborting;
-    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(aborting) : "r"(af) : "memory");
-    if (honor_abort && aborting) return false;
-    if (clock64() - t0 > limit) {
-      *abort_flag = 1;
-      report_status(status, MOE_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-
-// Every lane waits; the result is the same in all lanes, so the warp stays
-// converged for the .sync.aligned tcgen05 instructions that follow.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
-                                               volatile int* abort_flag, int* status,
-                                               bool honor_abort = true,
-                                               long long limit = kWaitCycles) {
-  const bool r = mbar_wait(bar, parity, abort_flag, status, honor_abort, limit);
-  return __all_sync(0xffffffffu, r);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* tm, int x, int y,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
 // The four MMAs of one 64-deep k-block (K-steps of 16) into one accumulator,
 // in a single statement: D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16 (fp16 or
 // bf16 operands, fp32 accumulation). A columns advance 8 per K-step, the B
@@ -272,9 +175,6 @@ __device__ __forceinline__ void mma_kblock(uint32_t d0, uint32_t a0, uint32_t bl
       : "r"(idesc), "r"(first)
       : "memory");
 }
-
-// address of barrier i of an array of 8-byte mbarriers at shared address base
-__device__ __forceinline__ uint32_t bar_at(uint32_t base, uint32_t i) { return base + 8u * i; }
 
 // D[tmem] (+)= A[smem] * B[smem]^T for one 64-deep k-block (four K-steps of
 // 16; both descriptors advance 32 bytes inside the 128-byte swizzle atom);
@@ -313,25 +213,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&a)[16]) {
         "=r"(a[14]), "=r"(a[15])
       : "r"(ta)
       : "memory");
-}
-
-// tcgen05.commit from one elected lane of a converged warp
-__device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
-      : "memory");
-}
-
-// K-major operand in shared memory, 128-byte swizzle, rows of 128 bytes,
-// 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1 << 16;              // leading byte offset (unused for swizzled K-major)
-  d |= (uint64_t)(1024 >> 4) << 32;    // stride byte offset
-  d |= (uint64_t)1 << 46;              // descriptor version for sm_100
-  d |= (uint64_t)2 << 61;              // SWIZZLE_128B
-  return d;
 }
 
 // M = 128, N = n, fp32 accumulate, both operands K-major; operand format
@@ -1382,45 +1263,6 @@ __global__ void wait_selftest_kernel(long long limit, int* status) {
 }
 
 // ------------------------------------------------------------------ host
-
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-// 2-D tiled map: inner extent `inner` elements (contiguous), `outer` rows of
-// `row_bytes`, box (box_inner, box_outer).
-static bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
-                     uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                     CUtensorMapSwizzle sw, uint32_t outer_step = 1) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_bytes};
-  // with an outer traversal stride of s the box spans box_outer rows and
-  // loads every s-th of them (box_outer / s rows)
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, outer_step};
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-static int num_sms() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
-}
 
 // raw weight-tile map over a stack of `rows` weight rows of K elements
 // (16-bit rows are bf16, or fp16 for an fp16 router weight)

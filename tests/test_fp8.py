@@ -188,7 +188,7 @@ def _check_matmul(y, a, sa, b, sb, dtype):
     assert np.isfinite(err).all() and (err <= bound).all(), float((err / bound).max())
 
 
-MATMUL_SIZES = [(1, 1, 16), (1, 128, 128), (2, 17, 48), (7, 200, 272), (8, 512, 7168),
+MATMUL_SIZES = [(1, 1, 16), (33, 20, 16), (1, 128, 128), (2, 17, 48), (7, 200, 272), (8, 512, 7168),
                 (9, 256, 384), (33, 1000, 2064), (64, 96, 128), (100, 333, 656), (128, 256, 256),
                 (129, 640, 1024), (300, 257, 512), (511, 1024, 1152)]
 
@@ -300,6 +300,21 @@ STAGES = [  # T, E, k, d, F, BM, skew
 @pytest.mark.parametrize("T,E,k,d,F,BM,skew", STAGES)
 def test_expert_stages_streaming(moe, T, E, k, d, F, BM, skew, act):
     out = _run_stages(moe, T, E, k, d, F, moe.REGIME_GEMV, BM, skew, act, T + E)
+    _check_stages(*out)
+    assert moe.device_status() == moe.OK
+
+
+STAGES_TC = [  # T, E, k, d, F, skew
+    (1, 8, 2, 128, 128, 0.0), (5, 4, 3, 256, 384, 0.0), (33, 16, 4, 384, 128, 0.0),
+    (300, 6, 2, 256, 128, 0.0), (200, 32, 4, 128, 256, 0.2), (129, 1, 1, 640, 256, 0.0),
+    (400, 3, 2, 1152, 640, 0.3), (37, 64, 8, 256, 128, 0.05)]
+
+
+@gpu
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+@pytest.mark.parametrize("T,E,k,d,F,skew", STAGES_TC)
+def test_expert_stages_tensor_cores(moe, T, E, k, d, F, skew, act):
+    out = _run_stages(moe, T, E, k, d, F, moe.REGIME_TC, 128, skew, act, T + E)
     _check_stages(*out)
     assert moe.device_status() == moe.OK
 
