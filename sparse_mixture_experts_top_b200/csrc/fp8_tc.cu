@@ -116,21 +116,30 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm,
       : "memory");
 }
 
-// 32 columns of this warp's 32 lanes, and the wait for them, in one statement
-// (the registers are written asynchronously until the wait)
-__device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
+// 32 columns of this warp's 32 lanes. The registers are written until the
+// wait, which takes them as operands, so that nothing reads them before it.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t ta, uint32_t (&a)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
-        "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
-        "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]),
-        "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]),
-        "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
       : "r"(ta)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&a)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+               :
+               : "memory");
+}
+
+// acc += d * f for two columns at a time
+__device__ __forceinline__ void fma2(float& x, float& y, uint32_t d0, uint32_t d1, float f) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "r"(d0), "r"(d1), "f"(f));
 }
 
 // 32 bytes to a 32-byte-aligned address: one whole sector per lane
@@ -424,20 +433,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p.wait_limit);
         if (!ok) break;
         tc_fence_after();
+        // a chunk of 32 columns is scaled while the next is on its way; the
+        // buffer is handed back as soon as the last has arrived
+        constexpr int NCH = COLS / 32, H = COLS / 2;
+        uint32_t d[2][32];
         if (live) {
+          tmem_ld32_start(tl + b * BN + c0, d[0]);
+          tmem_ld32_wait(d[0]);
+        }
 #pragma unroll
-          for (int j = 0; j < COLS; j += 32) {
-            constexpr int H = COLS / 2;
-            uint32_t d[32];
-            tmem_ld32(tl + b * BN + (j < H ? c0 + j : c1 + j - H), d);
+        for (int j = 0; j < NCH; ++j) {
+          if (live && j + 1 < NCH) {
+            const int c = (j + 1) * 32;
+            tmem_ld32_start(tl + b * BN + (c < H ? c0 + c : c1 + c - H), d[(j + 1) & 1]);
+          }
+          if (j + 1 == NCH) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
+          }
+          if (live) {
+            const float f = j * 32 < H ? f0 : f1;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              acc[j + i] = fmaf(__uint_as_float(d[i]), j < H ? f0 : f1, acc[j + i]);
+            for (int i = 0; i < 32; i += 2)
+              fma2(acc[j * 32 + i], acc[j * 32 + i + 1], d[j & 1][i], d[j & 1][i + 1], f);
+            if (j + 1 < NCH) tmem_ld32_wait(d[(j + 1) & 1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
       }
       if (!ok) break;
       if (MODE == MODE_STORE) {
