@@ -288,25 +288,33 @@ F8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 
 
-def _codes(t, what):
-    if t.dtype not in (F8, torch.uint8):
-        raise TypeError(f"{what} must be e4m3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+def _on(*ts):
+    """Contiguous tensors of the current device, where the launches go; the
+    raw handle of its current stream."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("inputs must be contiguous CUDA tensors")
+            if t.get_device() != dev:
+                raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _typed(t, dtype, shape, what):
-    if t.dtype != dtype or tuple(t.shape) != shape:
+def _is(t, dtype, shape, what):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _here(t, *others):
-    """The launches go to the current device: every tensor must be on it."""
-    dev = t.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    for o in others:
-        if o is not None and o.device != dev:
-            raise ValueError(f"tensors are on {dev} and {o.device}")
+def _codes(t, dims, what):
+    if t.dtype != F8 and t.dtype != torch.uint8:
+        raise TypeError(f"{what} must be e4m3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{what} must have {dims} dimensions, got {list(t.shape)}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def quantize_fp8(x, block=1, stream=None):
@@ -315,19 +323,23 @@ def quantize_fp8(x, block=1, stream=None):
     elements (block=128: [ceil(rows/128), ceil(K/128)], for weights). A stack of
     weights x [E, rows, K] (rows a multiple of 128 for block=128) gives a stack
     of scales."""
-    _dev(x)
-    _here(x)
+    raw = _on(x)
+    if x.dim() < 2:
+        raise ValueError(f"x must be [rows, K] or a stack of such, got {list(x.shape)}")
     *lead, rows, K = x.shape
-    if block not in (1, FP8_BLOCK):
+    if block != 1 and block != FP8_BLOCK:
         raise ValueError(f"block must be 1 or {FP8_BLOCK}, got {block}")
-    if lead and block != 1 and rows % FP8_BLOCK:
-        raise ValueError("a stack of weights needs rows in multiples of 128 (a block of "
-                         "scales may not straddle two of them)")
-    n = x.numel() // K if K else 0
-    q = torch.empty(x.shape, dtype=F8, device=x.device)
-    s = torch.empty(*lead, -(-rows // block), -(-K // FP8_BLOCK), dtype=torch.float32,
-                    device=x.device)
-    _check(lib.moe_quantize_fp8(_ptr(x), _dt(x), n, K, block, _ptr(q), _ptr(s), _stream(stream)),
+    n = rows
+    if lead:
+        if block != 1 and rows % FP8_BLOCK:
+            raise ValueError("a stack of weights needs rows in multiples of 128 (a block of "
+                             "scales may not straddle two of them)")
+        n = x.numel() // K if K else 0
+    q = torch.empty_like(x, dtype=F8)
+    s = x.new_empty((*lead, rows if block == 1 else -(-rows // FP8_BLOCK), -(-K // FP8_BLOCK)),
+                    dtype=torch.float32)
+    _check(lib.moe_quantize_fp8(x.data_ptr(), _dt(x), n, K, block, q.data_ptr(), s.data_ptr(),
+                                raw if stream is None else stream.cuda_stream),
            "moe_quantize_fp8")
     return q, s
 
@@ -335,62 +347,78 @@ def quantize_fp8(x, block=1, stream=None):
 def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
     """y [M, N] = a . b^T in `dtype` from e4m3 codes a [M, K], b [N, K] and fp32
     scales sa [M, ceil(K/128)], sb [ceil(N/128), ceil(K/128)]."""
-    _dev(a, sa, b, sb, out)
-    _here(a, sa, b, sb, out)
-    _codes(a, "a")
-    _codes(b, "b")
+    raw = _on(a, sa, b, sb, out)
+    _codes(a, 2, "a")
+    _codes(b, 2, "b")
     M, K = a.shape
-    N = b.shape[0]
+    N, KB = b.shape
+    if KB != K:
+        raise ValueError(f"a is [{M}, {K}] and b [{N}, {KB}]: K differs")
     KB = -(-K // FP8_BLOCK)
-    if b.shape[1] != K:
-        raise ValueError(f"a is [{M}, {K}] and b [{N}, {b.shape[1]}]: K differs")
-    _typed(sa, torch.float32, (M, KB), "sa")
-    _typed(sb, torch.float32, (-(-N // FP8_BLOCK), KB), "sb")
+    _is(sa, torch.float32, (M, KB), "sa")
+    _is(sb, torch.float32, (-(-N // FP8_BLOCK), KB), "sb")
     if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=a.device)
+        out = a.new_empty((M, N), dtype=dtype)
     else:
-        _typed(out, dtype, (M, N), "out")
-    _check(lib.moe_fp8_matmul(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), M, N, K, _dt_of(dtype),
-                              _ptr(out), _stream(stream)), "moe_fp8_matmul")
+        _is(out, dtype, (M, N), "out")
+    _check(lib.moe_fp8_matmul(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), M, N, K,
+                              _dt_of(dtype), out.data_ptr(),
+                              raw if stream is None else stream.cuda_stream), "moe_fp8_matmul")
     return out
+
+
+def _f8_experts(ex) -> Experts:
+    """C view of f8 experts, whose shapes the grouped calls rely on."""
+    fmt = ex.fmt
+    if (_FMT[fmt] if isinstance(fmt, str) else int(fmt)) == W_F8:
+        E, d, F, B = ex.E, ex.d, ex.F, FP8_BLOCK
+        if ex.w_gu.shape != (E, 2 * F, d) or ex.w_dn.shape != (E, d, F):
+            raise ValueError("f8 experts: w_gu must be [E, 2F, d] and w_dn [E, d, F]")
+        _is(ex.s_gu, torch.float32, (E, 2 * F // B, d // B), "s_gu")
+        _is(ex.s_dn, torch.float32, (E, d // B, F // B), "s_dn")
+    return experts_struct(ex)
 
 
 def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUTO, stream=None):
     """-> (hq e4m3 [T*k, F], hs fp32 [T*k, F/128]): gate|up and GLU of f8 experts
     from quantised token rows xq [T, d], xs [T, d/128] (quantize_fp8)."""
-    _dev(xq, xs)
-    _here(xq, xs, tables.row_map, experts.w_gu)
-    _codes(xq, "xq")
-    T = xq.shape[0]
-    _typed(xs, torch.float32, (T, experts.d // FP8_BLOCK), "xs")
-    if xq.shape[1] != experts.d:
+    rmap, roff, toff = tables.row_map, tables.row_off, tables.tile_off
+    raw = _on(xq, xs, rmap, roff, toff, experts.w_gu)
+    _codes(xq, 2, "xq")
+    T, d = xq.shape
+    if d != experts.d:
         raise ValueError(f"xq is {list(xq.shape)}, the experts' d is {experts.d}")
-    if tables.row_map.numel() != T * k:
-        raise ValueError(f"the tables are of {tables.row_map.numel()} rows, not {T} x {k}")
-    ex = experts_struct(experts)
-    hq = torch.empty(T * k, experts.F, dtype=F8, device=xq.device)
-    hs = torch.empty(T * k, -(-experts.F // FP8_BLOCK), dtype=torch.float32, device=xq.device)
-    _check(lib.moe_grouped_swiglu_fp8(_ptr(xq), _ptr(xs), _ptr(tables.row_map),
-                                      _ptr(tables.row_off), _ptr(tables.tile_off), tables.BM, T, k,
-                                      ctypes.byref(ex), _ptr(hq), _ptr(hs), regime,
-                                      _stream(stream)), "moe_grouped_swiglu_fp8")
+    _is(xs, torch.float32, (T, -(-d // FP8_BLOCK)), "xs")
+    R, F = T * k, experts.F
+    if rmap.numel() != R:
+        raise ValueError(f"the tables are of {rmap.numel()} rows, not {T} x {k}")
+    ex = _f8_experts(experts)
+    hq = xq.new_empty((R, F), dtype=F8)
+    hs = xs.new_empty((R, -(-F // FP8_BLOCK)))
+    _check(lib.moe_grouped_swiglu_fp8(xq.data_ptr(), xs.data_ptr(), rmap.data_ptr(),
+                                      roff.data_ptr(), toff.data_ptr(), tables.BM, T, k,
+                                      ctypes.byref(ex), hq.data_ptr(), hs.data_ptr(), regime,
+                                      raw if stream is None else stream.cuda_stream),
+           "moe_grouped_swiglu_fp8")
     return hq, hs
 
 
 def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AUTO, stream=None):
     """-> ys fp16 [T*k, d] from quantised rows hq [T*k, F], hs [T*k, F/128]
     (grouped_swiglu_fp8)."""
-    _dev(hq, hs)
-    _here(hq, hs, tables.row_off, experts.w_dn)
-    _codes(hq, "hq")
-    if tuple(hq.shape) != (T * k, experts.F):
-        raise ValueError(f"hq is {list(hq.shape)}, not [{T} x {k}, {experts.F}]")
-    _typed(hs, torch.float32, (T * k, experts.F // FP8_BLOCK), "hs")
-    ex = experts_struct(experts)
-    ys = torch.empty(T * k, experts.d, dtype=torch.float16, device=hq.device)
-    _check(lib.moe_grouped_down_fp8(_ptr(hq), _ptr(hs), _ptr(tables.row_off),
-                                    _ptr(tables.tile_off), tables.BM, T, k, ctypes.byref(ex),
-                                    _ptr(ys), regime, _stream(stream)), "moe_grouped_down_fp8")
+    roff, toff = tables.row_off, tables.tile_off
+    raw = _on(hq, hs, roff, toff, experts.w_dn)
+    _codes(hq, 2, "hq")
+    R, F = T * k, experts.F
+    if hq.shape != (R, F):
+        raise ValueError(f"hq is {list(hq.shape)}, not [{T} x {k}, {F}]")
+    _is(hs, torch.float32, (R, -(-F // FP8_BLOCK)), "hs")
+    ex = _f8_experts(experts)
+    ys = hs.new_empty((R, experts.d), dtype=torch.float16)
+    _check(lib.moe_grouped_down_fp8(hq.data_ptr(), hs.data_ptr(), roff.data_ptr(), toff.data_ptr(),
+                                    tables.BM, T, k, ctypes.byref(ex), ys.data_ptr(), regime,
+                                    raw if stream is None else stream.cuda_stream),
+           "moe_grouped_down_fp8")
     return ys
 
 
@@ -404,17 +432,17 @@ class BalanceStats:
     tokens: torch.Tensor    # int32 [sequences]
 
 
-def _balance_args(logits, mask, seq_off):
+def _balance_sizes(logits, mask, seq_off):
     if logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError(f"logits must be fp32 [T, E], got {logits.dtype} {list(logits.shape)}")
-    T = logits.shape[0]
-    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or
-                             tuple(mask.shape) != (T,)):
+    T, E = logits.shape
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (T,)):
         raise ValueError(f"mask must be bool or uint8 [{T}], got {mask.dtype} {list(mask.shape)}")
-    if seq_off is not None and (seq_off.dtype != torch.int32 or seq_off.dim() != 1 or
-                                seq_off.numel() < 2):
+    if seq_off is None:
+        return T, E, 1
+    if seq_off.dtype != torch.int32 or seq_off.dim() != 1 or seq_off.numel() < 2:
         raise ValueError("seq_off must be int32 [sequences + 1]")
-    return T, logits.shape[1], 1 if seq_off is None else seq_off.numel() - 1
+    return T, E, seq_off.numel() - 1
 
 
 def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
@@ -424,25 +452,25 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
     one where it is left out), from fp32 logits [T, E] and topk_idx int32 [T, k].
     mask [T]: tokens that are False take no part. ws: a uint8 tensor of
     moe_balance_loss_workspace bytes to reuse."""
-    _dev(logits, topk_idx, mask, seq_off)
-    _here(logits, topk_idx, mask, seq_off)
-    T, E, B = _balance_args(logits, mask, seq_off)
+    raw = _on(logits, topk_idx, mask, seq_off, ws)
+    T, E, B = _balance_sizes(logits, mask, seq_off)
     if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError(f"topk_idx must be int32 [{T}, k], got {topk_idx.dtype} "
                          f"{list(topk_idx.shape)}")
     k = topk_idx.shape[1]
-    dev = logits.device
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    counts = torch.empty(B, E, dtype=torch.int32, device=dev)
-    probs = torch.empty(B, E, dtype=torch.float32, device=dev)
-    tokens = torch.empty(B, dtype=torch.int32, device=dev)
+    loss = logits.new_empty(())
+    probs = logits.new_empty((B, E))
+    counts = topk_idx.new_empty((B, E))
+    tokens = topk_idx.new_empty((B,))
     if ws is None:
-        ws = torch.empty(lib.moe_balance_loss_workspace(T, E, B), dtype=torch.uint8, device=dev)
+        ws = logits.new_empty((lib.moe_balance_loss_workspace(T, E, B),), dtype=torch.uint8)
         if stream is not None:
             ws.record_stream(stream)     # freed here, still in use there
-    _check(lib.moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(mask), _ptr(seq_off), T, E, k, B,
-                                coef, _ptr(loss), _ptr(counts), _ptr(probs), _ptr(tokens),
-                                _ptr(ws), ws.numel(), _stream(stream)), "moe_balance_loss")
+    _check(lib.moe_balance_loss(logits.data_ptr(), topk_idx.data_ptr(), _at(mask), _at(seq_off), T,
+                                E, k, B, coef, loss.data_ptr(), counts.data_ptr(),
+                                probs.data_ptr(), tokens.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                raw if stream is None else stream.cuda_stream),
+           "moe_balance_loss")
     return BalanceStats(loss, counts, probs, tokens)
 
 
@@ -450,17 +478,19 @@ def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_o
                           dloss=None, stream=None):
     """-> dlogits fp32 [T, E], the gradient of balance_loss(logits, ..., coef, mask,
     seq_off) times dloss (an fp32 tensor of one value; 1 where it is left out)."""
-    _dev(logits, stats.counts, stats.tokens, mask, seq_off, dloss)
-    _here(logits, stats.counts, stats.tokens, mask, seq_off, dloss)
-    T, E, B = _balance_args(logits, mask, seq_off)
-    _typed(stats.counts, torch.int32, (B, E), "stats.counts")
-    _typed(stats.tokens, torch.int32, (B,), "stats.tokens")
+    counts, tokens = stats.counts, stats.tokens
+    raw = _on(logits, counts, tokens, mask, seq_off, dloss)
+    T, E, B = _balance_sizes(logits, mask, seq_off)
+    _is(counts, torch.int32, (B, E), "stats.counts")
+    _is(tokens, torch.int32, (B,), "stats.tokens")
     if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
         raise ValueError("dloss must be one fp32 value")
     d = torch.empty_like(logits)
-    _check(lib.moe_balance_loss_backward(_ptr(logits), _ptr(mask), _ptr(seq_off), T, E, k, B, coef,
-                                         _ptr(stats.counts), _ptr(stats.tokens), _ptr(dloss),
-                                         _ptr(d), _stream(stream)), "moe_balance_loss_backward")
+    _check(lib.moe_balance_loss_backward(logits.data_ptr(), _at(mask), _at(seq_off), T, E, k, B,
+                                         coef, counts.data_ptr(), tokens.data_ptr(), _at(dloss),
+                                         d.data_ptr(),
+                                         raw if stream is None else stream.cuda_stream),
+           "moe_balance_loss_backward")
     return d
 
 

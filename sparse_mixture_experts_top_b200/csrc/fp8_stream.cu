@@ -8,7 +8,8 @@
 // exact), then the block's sum is scaled and added in fp32.
 //
 // A CTA takes 16 weight rows (GLU: 16 gate and 16 up rows) and up to 8 token
-// rows at a time: its 8 warps share out the K blocks, so that even a narrow
+// rows at a time (a dense product of more rows: 32, so that the weights are
+// read a quarter as often): its 8 warps share out the K blocks, so that even a narrow
 // product has every block's loads in flight at once, and add their sums in
 // order through shared memory. The MMA sums over k in any order, so each lane
 // loads 16 consecutive codes of its row and feeds them as four registers of
@@ -62,13 +63,13 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The CTA's products of matrices of 16 weight rows (first row pointers wa,
-// scales wsc) with token rows [r0, r0 + nv), nv <= 8, left in
-// red[0][mat][row][token], summed over the warps in order.
-template <int MATS>
+// The CTA's products of MATS matrices of 16 weight rows (the lane's two rows at
+// wa, scales at wsc) with token rows [r0, r0 + nv), nv <= 8 NT, left in
+// red[warp][mat][row][token] by each warp.
+template <int MATS, int NT>
 __device__ __forceinline__ void tile_products(const Params& p, const uint8_t* const (&wa)[MATS][2],
                                               const float* const (&wsc)[MATS], int r0, int nv,
-                                              float (*red)[MATS][kRows][kTok]) {
+                                              float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   // rows past the tile repeat its last one; their results are not stored
@@ -76,70 +77,100 @@ __device__ __forceinline__ void tile_products(const Params& p, const uint8_t* co
     const int r = r0 + min(i, nv - 1);
     return p.row_map ? (size_t)__ldg(p.row_map + r) : (size_t)r;
   };
-  const uint8_t* xr = p.x + row_of(g) * p.K;
-  const float* s0 = p.xs + row_of(2 * c) * p.KB;
-  const float* s1 = p.xs + row_of(2 * c + 1) * p.KB;
-  float acc[MATS][4];
+  const uint8_t* xr[NT];
+  const float* sc[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    xr[t] = p.x + row_of(t * kTok + g) * p.K;
+    sc[t][0] = p.xs + row_of(t * kTok + 2 * c) * p.KB;
+    sc[t][1] = p.xs + row_of(t * kTok + 2 * c + 1) * p.KB;
+  }
+  float acc[MATS][NT][4];
 #pragma unroll
   for (int m = 0; m < MATS; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.f;
   const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-  for (int kb = warp; kb < p.KB; kb += kWarps) {
-    uint4 a[MATS][2][2], b[2];
+  // UN k-blocks' weights are loaded at once, before any token row is looked at
+  constexpr int UN = MATS == 1 && NT == 1 ? 4 : MATS == 1 ? 2 : 1;
+  for (int kb0 = warp; kb0 < p.KB; kb0 += kWarps * UN) {
+    uint4 a[UN][MATS][2][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k0 = kb * kBlock + h * 64 + c * 16;      // K % 16 == 0: all 16 codes or none
-      const bool in = k0 < p.K;
-      b[h] = in ? __ldg(reinterpret_cast<const uint4*>(xr + k0)) : z;
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        a[m][h][0] = in ? ldg_nc_v4(wa[m][0] + k0) : z;
-        a[m][h][1] = in ? ldg_nc_v4(wa[m][1] + k0) : z;
-      }
-    }
-    const float t0 = __ldg(s0 + kb), t1 = __ldg(s1 + kb);
-#pragma unroll
-    for (int m = 0; m < MATS; ++m) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < UN; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 &u = a[m][h][0], &v = a[m][h][1];
-        mma_e4m3(d, u.x, v.x, u.y, v.y, b[h].x, b[h].y);
-        mma_e4m3(d, u.z, v.z, u.w, v.w, b[h].z, b[h].w);
+        const int k0 = (kb0 + u * kWarps) * kBlock + h * 64 + c * 16;   // K % 16 == 0: all 16 or none
+        const bool in = k0 < p.K;
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          a[u][m][h][0] = in ? ldg_nc_v4(wa[m][0] + k0) : z;
+          a[u][m][h][1] = in ? ldg_nc_v4(wa[m][1] + k0) : z;
+        }
       }
-      const float sw = __ldg(wsc[m] + kb);
-      acc[m][0] = fmaf(d[0], sw * t0, acc[m][0]);
-      acc[m][1] = fmaf(d[1], sw * t1, acc[m][1]);
-      acc[m][2] = fmaf(d[2], sw * t0, acc[m][2]);
-      acc[m][3] = fmaf(d[3], sw * t1, acc[m][3]);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int kb = kb0 + u * kWarps;
+      if (kb >= p.KB) break;
+      float sw[MATS];
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) sw[m] = __ldg(wsc[m] + kb);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint4 b[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k0 = kb * kBlock + h * 64 + c * 16;
+          b[h] = k0 < p.K ? __ldg(reinterpret_cast<const uint4*>(xr[t] + k0)) : z;
+        }
+        const float t0 = __ldg(sc[t][0] + kb), t1 = __ldg(sc[t][1] + kb);
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 &v0 = a[u][m][h][0], &v1 = a[u][m][h][1];
+            mma_e4m3(d, v0.x, v1.x, v0.y, v1.y, b[h].x, b[h].y);
+            mma_e4m3(d, v0.z, v1.z, v0.w, v1.w, b[h].z, b[h].w);
+          }
+          acc[m][t][0] = fmaf(d[0], sw[m] * t0, acc[m][t][0]);
+          acc[m][t][1] = fmaf(d[1], sw[m] * t1, acc[m][t][1]);
+          acc[m][t][2] = fmaf(d[2], sw[m] * t0, acc[m][t][2]);
+          acc[m][t][3] = fmaf(d[3], sw[m] * t1, acc[m][t][3]);
+        }
+      }
     }
   }
 #pragma unroll
-  for (int m = 0; m < MATS; ++m) {
-    red[warp][m][g][2 * c] = acc[m][0];
-    red[warp][m][g][2 * c + 1] = acc[m][1];
-    red[warp][m][g + 8][2 * c] = acc[m][2];
-    red[warp][m][g + 8][2 * c + 1] = acc[m][3];
-  }
+  for (int m = 0; m < MATS; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float* o = red + ((warp * MATS + m) * NT + t) * (kRows * kTok);
+      *reinterpret_cast<float2*>(o + g * kTok + 2 * c) = make_float2(acc[m][t][0], acc[m][t][1]);
+      *reinterpret_cast<float2*>(o + (g + 8) * kTok + 2 * c) =
+          make_float2(acc[m][t][2], acc[m][t][3]);
+    }
   __syncthreads();
 }
 
-template <int MATS>
-__device__ __forceinline__ float sum_warps(float (*red)[MATS][kRows][kTok], int m, int row, int tok) {
-  float v = red[0][m][row][tok];
+// the warps' sums added in order
+template <int MATS, int NT>
+__device__ __forceinline__ float sum_warps(const float* red, int m, int row, int tok) {
+  const float* o = red + (m * NT + tok / kTok) * (kRows * kTok) + row * kTok + tok % kTok;
+  float v = o[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) v += red[w][m][row][tok];
+  for (int w = 1; w < kWarps; ++w) v += o[w * MATS * NT * kRows * kTok];
   return v;
 }
 
 // Rows [r0, r0 + nv) and expert of tile `tau`; false past the last tile.
+template <int NT>
 __device__ __forceinline__ bool tile_rows(const Params& p, int tau, int& e, int& r0, int& nv) {
   if (!p.row_off) {
     e = 0;
-    r0 = tau * kTok;
-    nv = min(kTok, p.M - r0);
+    r0 = tau * NT * kTok;
+    nv = min(NT * kTok, p.M - r0);
     return nv > 0;
   }
   if (tau >= __ldg(p.tile_off + p.E)) return false;
@@ -150,26 +181,28 @@ __device__ __forceinline__ bool tile_rows(const Params& p, int tau, int& e, int&
 }
 
 // Columns n0..n0+15 of y, for the rows of the tiles blockIdx.y, + gridDim.y, ...
-__global__ void __launch_bounds__(kThreads) stream_store_kernel(const Params p) {
-  __shared__ float red[kWarps][1][kRows][kTok];
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 2) stream_store_kernel(const Params p) {
+  __shared__ __align__(16) float red[kWarps * NT * kRows * kTok];
   pdl_wait();
   pdl_launch();
   const int n0 = blockIdx.x * kRows;
   const int g = (threadIdx.x & 31) >> 2;
-  const int row = threadIdx.x & 15, tok = threadIdx.x >> 4;      // threads 0..127
   bool over = false;
   for (int tau = blockIdx.y;; tau += gridDim.y) {
     int e, r0, nv;
-    if (!tile_rows(p, tau, e, r0, nv)) break;
+    if (!tile_rows<NT>(p, tau, e, r0, nv)) break;
     const uint8_t* we = p.w + (size_t)e * p.rows_per_group * p.K;
     // rows past N repeat the last one; their results are not stored
     const uint8_t* const wa[1][2] = {{we + (size_t)min(n0 + g, p.N - 1) * p.K,
                                       we + (size_t)min(n0 + g + 8, p.N - 1) * p.K}};
     const float* const wsc[1] = {p.ws + ((size_t)e * p.scale_rows + n0 / kBlock) * p.KB};
-    for (int i = 0; i < nv; i += kTok) {
-      tile_products<1>(p, wa, wsc, r0 + i, min(kTok, nv - i), red);
-      if (threadIdx.x < kRows * kTok && i + tok < nv && n0 + row < p.N) {
-        const float v = sum_warps<1>(red, 0, row, tok);
+    for (int i = 0; i < nv; i += NT * kTok) {
+      tile_products<1, NT>(p, wa, wsc, r0 + i, min(NT * kTok, nv - i), red);
+      for (int o = threadIdx.x; o < NT * kTok * kRows; o += kThreads) {
+        const int row = o % kRows, tok = o / kRows;
+        if (i + tok >= nv || n0 + row >= p.N) continue;
+        const float v = sum_warps<1, NT>(red, 0, row, tok);
         const size_t at = (size_t)(r0 + i + tok) * p.N + n0 + row;
         if (p.out_dt == MOE_F16) {
           const __half h = __float2half_rn(v);
@@ -188,9 +221,9 @@ __global__ void __launch_bounds__(kThreads) stream_store_kernel(const Params p) 
 }
 
 // Features f0..f0+15 of h = act(g) * u, quantised over the cluster's 128.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 3)
     stream_glu_kernel(const Params p) {
-  __shared__ float red[kWarps][2][kRows][kTok];
+  __shared__ __align__(16) float red[kWarps * 2 * kRows * kTok];
   __shared__ float s_max[2][kTok];
   pdl_wait();
   pdl_launch();
@@ -201,18 +234,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   unsigned it = 0;
   for (int tau = blockIdx.y;; tau += gridDim.y) {
     int e, r0, nv;
-    if (!tile_rows(p, tau, e, r0, nv)) break;       // the same in all CTAs of the cluster
+    if (!tile_rows<1>(p, tau, e, r0, nv)) break;    // the same in all CTAs of the cluster
     const uint8_t* wg = p.w + ((size_t)e * p.rows_per_group + f0 + g) * p.K;
     const uint8_t* wu = wg + (size_t)p.N * p.K;
     const uint8_t* const wa[2][2] = {{wg, wg + (size_t)8 * p.K}, {wu, wu + (size_t)8 * p.K}};
     const float* sg = p.ws + ((size_t)e * p.scale_rows + f0 / kBlock) * p.KB;
     const float* const wsc[2] = {sg, sg + (size_t)(p.N / kBlock) * p.KB};
     for (int i = 0; i < nv; i += kTok, ++it) {
-      tile_products<2>(p, wa, wsc, r0 + i, min(kTok, nv - i), red);
+      tile_products<2, 1>(p, wa, wsc, r0 + i, min(kTok, nv - i), red);
       float h = 0.f;
       float(*mx)[kTok] = s_max + (it & 1);
       if (threadIdx.x < kRows * kTok) {
-        h = glu(p.act, sum_warps<2>(red, 0, row, tok), sum_warps<2>(red, 1, row, tok));
+        h = glu(p.act, sum_warps<2, 1>(red, 0, row, tok), sum_warps<2, 1>(red, 1, row, tok));
         float m = finite_abs(h);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -260,8 +293,12 @@ cudaError_t launch_fp8_matmul_stream(const void* a, const float* sa, const void*
   p.out = y;
   p.out_dt = out_dt;
   p.status = status;
-  const dim3 grid((unsigned)((N + kRows - 1) / kRows), grid_y(((long long)M + kTok - 1) / kTok));
-  launch_pdl(stream_store_kernel, grid, kThreads, 0, s, p);
+  const unsigned gx = (unsigned)((N + kRows - 1) / kRows);
+  auto gy = [&](int nt) { return grid_y(((long long)M + nt * kTok - 1) / (nt * kTok)); };
+  if (M <= 8)
+    launch_pdl(stream_store_kernel<1>, dim3(gx, gy(1)), kThreads, 0, s, p);
+  else
+    launch_pdl(stream_store_kernel<4>, dim3(gx, gy(4)), kThreads, 0, s, p);
   return cudaGetLastError();
 }
 
@@ -316,7 +353,7 @@ cudaError_t launch_down_fp8_stream(const void* hq, const float* hs, const int32_
   p.out_dt = MOE_F16;
   p.status = status;
   const dim3 grid((unsigned)(ex.d / kRows), grid_y(max_tiles(R, ex.E, BM)));
-  launch_pdl(stream_store_kernel, grid, kThreads, 0, s, p);
+  launch_pdl(stream_store_kernel<1>, grid, kThreads, 0, s, p);
   return cudaGetLastError();
 }
 

@@ -9,7 +9,7 @@
 // k-block. The MMA's accumulator cannot take a factor per row and block, so
 // each k-block's products go to a TMEM buffer of their own, and eight warps
 // read it back, scale it and add it to fp32 registers while the tensor core
-// fills the other buffer. With token rows on the lanes, the factor
+// fills the next buffer. With token rows on the lanes, the factor
 // xs[m][kb] ws[.][kb] is one value per thread and 64 columns: one FMA per element.
 //
 // Warps: 0 loads (TMA: weight boxes of 128 rows; token rows in boxes of 32, or,
@@ -23,7 +23,18 @@
 // quantised in the same epilogue, its block's largest magnitude exchanged
 // between the two halves through shared memory.
 //
-// Every mbarrier wait is bounded, as in the other tensor-core kernels.
+// Two forms:
+//   * persistent (one CTA per SM, BN = 256): units enough to go round;
+//   * split (BN = 128; gate|up 256): few units. A cluster of up to eight CTAs
+//     shares a unit's K blocks; each leaves its sums in its shared memory, and
+//     each then adds a share of the rows over the cluster, in rank order, and
+//     stores them: all SMs stream weights, and the result stays the same from
+//     run to run.
+//
+// Every mbarrier wait is bounded, as in the other tensor-core kernels; the
+// cluster barriers are reached by every thread, whatever the waits did.
+#include <cooperative_groups.h>
+
 #include "fp8.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
@@ -44,16 +55,21 @@ constexpr int A_BOX = 32;               // token rows per TMA box
 
 enum { MODE_STORE = 0, MODE_GLU = 1 };
 
-template <int BN> struct Cfg {
+template <int BN, bool SPLIT> struct Cfg {
   static constexpr int B_BYTES = BN * kBlock;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NS = BN == 256 ? 4 : 6;
+  static constexpr int NBUF = 512 / BN;             // accumulator buffers
   static constexpr int COLS = BN / 2;               // columns per scaling warp
-  static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int BARS = 256;
   static constexpr int AMAX = 2 * 2 * BM * 4;       // [tile parity][half][row]
   static constexpr int TABLES = 2 * (kMaxE + 1) * 4;
-  static constexpr int SMEM = 1024 + NS * STAGE + BARS + AMAX + TABLES;
+  static constexpr int PATCH_LD = 17;               // 32 rows x 16 columns of one warp
+  static constexpr int PATCH = SPLIT ? 0 : kAccWarps * 32 * PATCH_LD * 4;
+  static constexpr int SMEM = 1024 + NS * STAGE + BARS + AMAX + TABLES + PATCH + 16;
+  // split: the CTA's sums, in the ring once its last MMA is done
+  static constexpr int SUM_LD = BN + 4;             // rows 4 banks apart: 16-byte stores
+  static_assert(!SPLIT || BM * SUM_LD * 4 <= NS * STAGE, "the sums fit the ring");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -66,6 +82,7 @@ struct Params {
   int N;                     // output columns (GLU: features F)
   int K, KB;
   int n_units;               // units per token tile
+  int split;                 // CTAs that share a unit's K blocks (1: persistent form)
   const float* ws;           // [E][scale_rows][KB]
   int rows_per_group, scale_rows;
   void* out;
@@ -186,27 +203,53 @@ __device__ __forceinline__ Unit decode(const Params& p, const int* s_toff, const
   return r;
 }
 
-// One output row's COLS consecutive columns from column c of N, rounded to out_dt.
-template <int COLS>
-__device__ __forceinline__ void store_row(const Params& p, size_t row, int c, const float (&acc)[COLS],
-                                          bool& over) {
-  const size_t at = row * p.N + c;
+// One value, rounded to the output type.
+__device__ __forceinline__ void store_one(const Params& p, size_t at, float v, bool& over) {
+  if (p.out_dt == MOE_F16) {
+    const __half h = __float2half_rn(v);
+    over |= (__half_as_ushort(h) & 0x7FFFu) >= 0x7C00u;
+    reinterpret_cast<__half*>(p.out)[at] = h;
+  } else if (p.out_dt == MOE_BF16) {
+    reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  } else {
+    reinterpret_cast<float*>(p.out)[at] = v;
+  }
+}
+
+// A lane's output row: COLS consecutive columns from column c of N. Where every
+// row starts on a 32-byte boundary each lane stores whole sectors of its row;
+// elsewhere 16 columns at a time go through shared memory (the warp's patch),
+// and half a warp stores those of one row.
+template <int COLS, int LD>
+__device__ __forceinline__ void store_rows(const Params& p, int r0, int m0, int nv, int c,
+                                           const float (&acc)[COLS], float* patch, bool& over) {
+  const int lane = threadIdx.x & 31;
+  const int m = m0 + lane;
+  if (!p.wide) {
+#pragma unroll
+    for (int j = 0; j < COLS; j += 16) {
+      if (c + j >= p.N) break;                     // the same in the whole warp
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) patch[lane * LD + i] = acc[j + i];
+      __syncwarp();
+      const int col = c + j + (lane & 15);
+      for (int r = lane >> 4; r < 32 && m0 + r < nv; r += 2)
+        if (col < p.N)
+          store_one(p, ((size_t)r0 + m0 + r) * p.N + col, patch[r * LD + (lane & 15)], over);
+    }
+    return;
+  }
+  if (m >= nv) return;
+  const size_t at = ((size_t)r0 + m) * p.N + c;
   if (p.out_dt == MOE_F32) {
     float* o = reinterpret_cast<float*>(p.out) + at;
-    if (p.wide) {
 #pragma unroll
-      for (int j = 0; j < COLS; j += 8) {
-        if (c + j < p.N) {
-          uint32_t v[8];
+    for (int j = 0; j < COLS; j += 8) {
+      uint32_t v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(acc[j + i]);
-          st32(o + j, v);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < COLS; ++j)
-        if (c + j < p.N) o[j] = acc[j];
+      for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(acc[j + i]);
+      if (c + j < p.N) st32(o + j, v);
     }
     return;
   }
@@ -215,52 +258,92 @@ __device__ __forceinline__ void store_row(const Params& p, size_t row, int c, co
   uint32_t hmax = 0;
 #pragma unroll
   for (int j = 0; j < COLS; j += 16) {
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = acc[j + 2 * i], b = acc[j + 2 * i + 1];
-      v[i] = f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-    }
-    if (p.wide) {
-      if (c + j < p.N) st32(o + j, v);
-    } else {
+    if (c + j < p.N) {                             // N % 16 == 0
+      uint32_t v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (c + j + 2 * i < p.N) o[j + 2 * i] = (uint16_t)v[i];
-        if (c + j + 2 * i + 1 < p.N) o[j + 2 * i + 1] = (uint16_t)(v[i] >> 16);
+        const float a = acc[j + 2 * i], b = acc[j + 2 * i + 1];
+        v[i] = f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+        hmax = max(hmax, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
       }
-    }
-    // columns past N repeat nothing of the product's rows (zero-filled) or are
-    // another expert's: they are not looked at
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c + j + 2 * i < p.N) hmax = max(hmax, v[i] & 0x7FFFu);
-      if (c + j + 2 * i + 1 < p.N) hmax = max(hmax, (v[i] >> 16) & 0x7FFFu);
+      st32(o + j, v);
     }
   }
   over |= f16 && hmax >= 0x7C00u;
 }
 
-template <int MODE, int BN>
+// Split form: the sums of rows [0, nv) of the unit over the cluster's CTAs, a
+// warp per row, and their storage. Every CTA takes a share of the rows.
+template <int MODE, int BN, int LD>
+__device__ __forceinline__ void join_rows(const Params& p, const Unit& t, float* sums, int rank,
+                                          bool& over) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  constexpr int V = BN / 32;               // columns per lane
+  const int warp = (threadIdx.x >> 5) - kAccWarp0, lane = threadIdx.x & 31;
+  for (int r = rank * kAccWarps + warp; r < t.nv; r += p.split * kAccWarps) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+    for (int k = 0; k < p.split; ++k) {
+      const float* s = cluster.map_shared_rank(sums, k) + r * LD;
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        // runs of 128 columns: gate|up holds 4 gate and their 4 up columns
+        const float4 f = *reinterpret_cast<const float4*>(s + i * 32 + lane * 4);
+        v[i] += f.x;
+        v[i + 1] += f.y;
+        v[i + 2] += f.z;
+        v[i + 3] += f.w;
+      }
+    }
+    const size_t row = (size_t)t.r0 + r;
+    if constexpr (MODE == MODE_GLU) {
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = glu(p.act, v[i], v[4 + i]);
+        mx = fmaxf(mx, finite_abs(v[i]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float f = rscale_of(mx);
+      const size_t at = row * p.N + t.unit * kBlock + lane * 4;
+      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.out) + at) =
+          e4m3x4(code_arg(v[0], f), code_arg(v[1], f), code_arg(v[2], f), code_arg(v[3], f));
+      if (lane == 0) p.out_s[row * (p.N / kBlock) + t.unit] = scale_of(mx);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int col = t.unit * BN + (i / 4) * 128 + lane * 4 + i % 4;
+        if (col < p.N) store_one(p, row * p.N + col, v[i], over);
+      }
+    }
+  }
+}
+
+template <int MODE, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmA,
                   const __grid_constant__ CUtensorMap tmB) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, SPLIT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   const uint32_t st_base = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);   // [NS]
   uint64_t* empty = full + C::NS;                                          // [NS]
-  uint64_t* acc_full = empty + C::NS;                                      // [2]
-  uint64_t* acc_empty = acc_full + 2;                                      // [2]
-  uint64_t* xchg = acc_empty + 2;                                          // [1]
+  uint64_t* acc_full = empty + C::NS;                                      // [NBUF]
+  uint64_t* acc_empty = acc_full + C::NBUF;                                // [NBUF]
+  uint64_t* xchg = acc_empty + C::NBUF;                                    // [1]
   uint64_t* drain = xchg + 1;                                              // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_amax = reinterpret_cast<float*>(smem + C::NS * C::STAGE + C::BARS);
   int* s_toff = reinterpret_cast<int*>(smem + C::NS * C::STAGE + C::BARS + C::AMAX);
   int* s_roff = s_toff + kMaxE + 1;
+  float* s_patch = reinterpret_cast<float*>(
+      smem + C::NS * C::STAGE + C::BARS + C::AMAX + ((C::TABLES + 15) & ~15));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -269,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(full + i), 1);
       mbar_init(smem_u32(empty + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(smem_u32(acc_full + i), 1);
       mbar_init(smem_u32(acc_empty + i), kAccWarps);
     }
@@ -283,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
-                 "n"(C::TMEM)
+                 "n"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -300,6 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = total_units(p, s_toff);
+  // the CTA's units, and its share of their K blocks
+  const int rank = SPLIT ? (int)(blockIdx.x % (unsigned)p.split) : 0;
+  const int u0 = SPLIT ? (int)(blockIdx.x / (unsigned)p.split) : (int)blockIdx.x;
+  const int u_step = SPLIT ? total : (int)gridDim.x;      // split: one unit
+  const int kb_lo = SPLIT ? (int)((long long)p.KB * rank / p.split) : 0;
+  const int kb_hi = SPLIT ? (int)((long long)p.KB * (rank + 1) / p.split) : p.KB;
 
   if (warp < kAccWarp0) {
     regs_dec<72>();
@@ -307,14 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- loads (TMA)
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      for (int u = u0; u < total && ok; u += u_step) {
         const Unit t = decode(p, s_toff, s_roff, u);
         const int wrow = t.e * p.rows_per_group + t.unit * (MODE == MODE_GLU ? kBlock : BN);
         // boxes of weight rows that the product has (the rest of the stage
         // keeps old codes, whose columns are not stored)
-        const int boxes = MODE == MODE_GLU ? 2 : BN < kBlock ? 1
-                          : min(BN, p.N - t.unit * BN) > kBlock ? 2 : 1;
-        constexpr int BOX_BYTES = (BN < kBlock ? BN : kBlock) * kBlock;
+        const int boxes = MODE == MODE_GLU ? 2 : min(BN, p.N - t.unit * BN) > kBlock ? 2 : 1;
+        constexpr int BOX_BYTES = kBlock * kBlock;
         const int up = MODE == MODE_GLU ? p.N : kBlock;       // second box's row offset
         int rows[4] = {0, 0, 0, 0};
         int a_bytes;
@@ -328,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           a_bytes = (t.nv + A_BOX - 1) / A_BOX * (A_BOX * kBlock);
         }
-        for (int kb = 0; kb < p.KB && ok; ++kb, ++it) {
+        for (int kb = kb_lo; kb < kb_hi && ok; ++kb, ++it) {
           const uint32_t s = it % C::NS;
           if (it >= (uint32_t)C::NS) {
             ok = mbar_wait_warp(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
@@ -366,13 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_e4m3(BN);
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
-          const uint32_t s = it % C::NS, b = it & 1;
-          // buffer b was read back two k-blocks ago
-          if (it >= 2)
-            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it >> 1) - 1) & 1, abort_flag, p.status,
-                                true, p.wait_limit);
+      for (int u = u0; u < total && ok; u += u_step) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+          const uint32_t s = it % C::NS, b = it % C::NBUF;
+          // buffer b was read back NBUF k-blocks ago
+          if (it >= (uint32_t)C::NBUF)
+            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
+                                p.status, true, p.wait_limit);
           if (!ok) break;
           ok = mbar_wait_warp(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
                               p.wait_limit);
@@ -387,6 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_warp(smem_u32(drain));
       mbar_wait_warp(smem_u32(drain), 0, abort_flag, p.status, false);
     }
+    if constexpr (SPLIT) {
+      cooperative_groups::this_cluster().sync();     // the two barriers of the joining warps
+      cooperative_groups::this_cluster().sync();
+    }
   } else {
     // ------------------------------------------------------------ scale, add, store
     regs_inc<216>();
@@ -399,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c1 = MODE == MODE_GLU ? BN / 2 + c0 : c0 + COLS / 2;
     uint32_t it = 0, tiles = 0;
     bool ok = true, over = false;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++tiles) {
+    for (int u = u0; u < total && ok; u += u_step, ++tiles) {
       const Unit t = decode(p, s_toff, s_roff, u);
       const bool live = q * 32 < t.nv;            // some of the warp's lanes are rows
       const int m = q * 32 + lane;
@@ -420,16 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      float a = __ldg(sa), b0 = __ldg(w0), b1 = __ldg(w1);
-      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+      float a = __ldg(sa + kb_lo), b0 = __ldg(w0 + kb_lo), b1 = __ldg(w1 + kb_lo);
+      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const float f0 = a * b0, f1 = a * b1;
-        if (kb + 1 < p.KB) {                      // the next block's, ahead of the wait
+        if (kb + 1 < kb_hi) {                     // the next block's, ahead of the wait
           a = __ldg(sa + kb + 1);
           b0 = __ldg(w0 + kb + 1);
           b1 = __ldg(w1 + kb + 1);
         }
-        const uint32_t b = it & 1;
-        ok = mbar_wait_warp(smem_u32(acc_full + b), (it >> 1) & 1, abort_flag, p.status, true,
+        const uint32_t b = it % C::NBUF;
+        ok = mbar_wait_warp(smem_u32(acc_full + b), (it / C::NBUF) & 1, abort_flag, p.status, true,
                             p.wait_limit);
         if (!ok) break;
         tc_fence_after();
@@ -462,8 +554,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (MODE == MODE_STORE) {
-        if (m < t.nv) store_row<COLS>(p, (size_t)t.r0 + m, t.unit * BN + c0, acc, over);
+      if constexpr (SPLIT) {
+        // every MMA of this CTA is done and every load consumed: the ring is free
+        constexpr int H = COLS / 2;
+        float* o = reinterpret_cast<float*>(smem) + m * C::SUM_LD;
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < COLS; j += 4)
+            *reinterpret_cast<float4*>(o + (j < H ? c0 + j : c1 + j - H)) =
+                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        }
+      } else if constexpr (MODE == MODE_STORE) {
+        if (live)
+          store_rows<COLS, C::PATCH_LD>(p, t.r0, q * 32, t.nv, t.unit * BN + c0, acc,
+                                        s_patch + (warp - kAccWarp0) * 32 * C::PATCH_LD, over);
       } else {
         constexpr int H = COLS / 2;
         float mx = 0.f;
@@ -507,44 +611,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if constexpr (SPLIT) {
+      cooperative_groups::this_cluster().sync();     // every CTA's sums are in place
+      // (a CTA that gave up waiting has left none; the status says so)
+      if (u0 < total)
+        join_rows<MODE, BN, C::SUM_LD>(p, decode(p, s_toff, s_roff, u0),
+                                       reinterpret_cast<float*>(smem), rank, over);
+      cooperative_groups::this_cluster().sync();     // no CTA leaves while its sums are read
+    }
     if (MODE == MODE_STORE && over) report_status(p.status, MOE_ERR_RANGE);
   }
-
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::TMEM)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512)
                  : "memory");
   }
 }
 
 // ------------------------------------------------------------------ host
 
-template <int MODE, int BN>
+template <int MODE, int BN, bool SPLIT>
+static cudaError_t launch(const Params& p, const CUtensorMap& ta, const CUtensorMap& tb,
+                          unsigned grid, cudaStream_t s) {
+  auto kern = fp8_tc_kernel<MODE, BN, SPLIT>;
+  constexpr int smem = Cfg<BN, SPLIT>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = kThreads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p, ta, tb);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// tiles: token tiles at most. The split form is taken where the persistent
+// one's units would not fill half of the SMs; its clusters grow while the CTAs
+// fit the SMs and each keeps four K blocks or more.
+template <int MODE>
 static cudaError_t run(Params& p, const void* x, long long x_rows, const void* w, long long tiles,
                        cudaStream_t s) {
-  p.n_units = MODE == MODE_GLU ? p.N / kBlock : (p.N + BN - 1) / BN;
+  constexpr int BNS = MODE == MODE_GLU ? 256 : 128;          // columns of the split form
   p.wait_limit = wait_cycles();
   const int esize = MODE == MODE_GLU ? 1 : p.out_dt == MOE_F32 ? 4 : 2;
   p.wide = (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) && ((long long)p.N * esize) % 32 == 0;
   // rows are addressed by 32-bit coordinates
   if ((long long)p.E * p.rows_per_group > 0x7fffffffLL) return cudaErrorNotSupported;
   CUtensorMap ta, tb;
-  const uint32_t wbox = BN < kBlock ? BN : kBlock;
   if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, p.K, (uint64_t)x_rows, p.K, kBlock,
                 p.row_map ? 1 : A_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.K, (uint64_t)p.E * p.rows_per_group, p.K,
-                kBlock, wbox, CU_TENSOR_MAP_SWIZZLE_128B))
+                kBlock, kBlock, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(fp8_tc_kernel<MODE, BN>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
-  if (e != cudaSuccess) return e;
+  const int sms = num_sms();
+  const int per_tile = MODE == MODE_GLU ? p.N / kBlock : (p.N + 255) / 256;
+  if (tiles * per_tile * 2 > sms) {
+    p.n_units = per_tile;
+    p.split = 1;
+    const long long units = tiles * per_tile;
+    if (units > 0x7fffffffLL) return cudaErrorNotSupported;
+    return launch<MODE, 256, false>(p, ta, tb, units < sms ? (unsigned)units : (unsigned)sms, s);
+  }
+  p.n_units = MODE == MODE_GLU ? p.N / kBlock : (p.N + BNS - 1) / BNS;
   const long long units = tiles * p.n_units;
-  if (units > 0x7fffffffLL) return cudaErrorNotSupported;
-  const int grid = units < num_sms() ? (int)units : num_sms();
-  launch_pdl(fp8_tc_kernel<MODE, BN>, (unsigned)grid, kThreads, Cfg<BN>::SMEM, s, p, ta, tb);
-  return cudaGetLastError();
+  p.split = 1;
+  while (p.split < 8 && units * p.split * 2 <= sms && p.KB >= p.split * 8) p.split *= 2;
+  return launch<MODE, BNS, true>(p, ta, tb, (unsigned)(units * p.split), s);
 }
 
 }  // namespace fp8tc
@@ -566,7 +710,7 @@ cudaError_t launch_fp8_matmul_tc(const void* a, const float* sa, const void* b, 
   p.out = y;
   p.out_dt = out_dt;
   p.status = status;
-  return run<MODE_STORE, 256>(p, a, M, b, ((long long)M + BM - 1) / BM, s);
+  return run<MODE_STORE>(p, a, M, b, ((long long)M + BM - 1) / BM, s);
 }
 
 cudaError_t launch_swiglu_fp8_tc(const void* xq, const float* xs, int T, const uint32_t* row_map,
@@ -591,7 +735,7 @@ cudaError_t launch_swiglu_fp8_tc(const void* xq, const float* xs, int T, const u
   p.out_s = hs;
   p.act = ex.act;
   p.status = status;
-  return run<MODE_GLU, 256>(p, xq, T, ex.w_gu, max_tiles(R, ex.E, BM), s);
+  return run<MODE_GLU>(p, xq, T, ex.w_gu, max_tiles(R, ex.E, BM), s);
 }
 
 cudaError_t launch_down_fp8_tc(const void* hq, const float* hs, const int32_t* row_off,
@@ -613,7 +757,7 @@ cudaError_t launch_down_fp8_tc(const void* hq, const float* hs, const int32_t* r
   p.out = ys;
   p.out_dt = MOE_F16;
   p.status = status;
-  return run<MODE_STORE, 256>(p, hq, R, ex.w_dn, max_tiles(R, ex.E, BM), s);
+  return run<MODE_STORE>(p, hq, R, ex.w_dn, max_tiles(R, ex.E, BM), s);
 }
 
 }  // namespace moe
