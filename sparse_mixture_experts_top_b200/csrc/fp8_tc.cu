@@ -12,9 +12,11 @@
 // fills the next buffer. With token rows on the lanes, the factor
 // xs[m][kb] ws[.][kb] is one value per thread and 64 columns: one FMA per element.
 //
-// Warps: 0 loads (TMA: weight boxes of 128 rows; token rows in boxes of 32, or,
-// through row_map, four rows per gather), 1 issues the MMAs, 4..11 scale, add
-// and store: warp w reads TMEM lanes 32 (w % 4) .., and half (w - 4) / 4 of the
+// Warps: 0 loads by TMA (a stage's weight rows in one copy, its token rows in
+// another: every further copy of a stage cost about 65 cycles), 1 issues the
+// MMAs, 2 and 3 gather token rows through row_map (16-byte asynchronous copies
+// into the same swizzled layout; TMA's four-row gathers were slower), 4..11
+// scale, add and store: warp w reads TMEM lanes 32 (w % 4) .., and half (w - 4) / 4 of the
 // columns. Register shares: 72 per thread for warps 0..3, 216 for warps 4..11
 // (their sums of up to 128 columns live in registers), 168 at launch.
 //
@@ -51,9 +53,13 @@ constexpr int kThreads = 384;
 constexpr int kAccWarp0 = 4;
 constexpr int kAccWarps = 8;
 constexpr int A_BYTES = BM * kBlock;
-constexpr int A_BOX = 32;               // token rows per TMA box
+// token rows of a tile's copy: the least of these that holds it
+constexpr int A_MAPS = 3;
+__host__ __device__ constexpr int a_rows(int i) { return 32 << i; }
+constexpr int kGatherThreads = 64;      // warps 2 and 3
+constexpr int kGatherLag = 2;           // stages a gatherer runs ahead of its arrivals
 
-enum { MODE_STORE = 0, MODE_GLU = 1 };
+enum { MODE_STORE = 0, MODE_SWIGLU = 1, MODE_GEGLU = 2 };   // (the gate's activation)
 
 template <int BN, bool SPLIT> struct Cfg {
   static constexpr int B_BYTES = BN * kBlock;
@@ -71,9 +77,14 @@ template <int BN, bool SPLIT> struct Cfg {
   static constexpr int SUM_LD = BN + 4;             // rows 4 banks apart: 16-byte stores
   static_assert(!SPLIT || BM * SUM_LD * 4 <= NS * STAGE, "the sums fit the ring");
   static_assert(SMEM <= 232448, "shared memory per CTA");
+  static_assert(kGatherLag < NS, "a gathered stage is handed over before its ring slot is due");
 };
 
 struct Params {
+  CUtensorMap tmA[A_MAPS];   // token rows [.][K]: boxes of 128 x a_rows(i)
+  CUtensorMap tmB;           // weight rows: a stage's box (gate|up: 3-D, both blocks)
+  CUtensorMap tmB1;          // 128 rows: a last unit of at most 128 columns
+  const uint8_t* x;          // token codes, for the gather
   const float* xs;           // [.][KB] scales of the token rows
   const uint32_t* row_map;   // GLU: token row of each sorted row
   const int32_t* row_off;    // null: one dense product of M rows
@@ -87,7 +98,7 @@ struct Params {
   int rows_per_group, scale_rows;
   void* out;
   float* out_s;              // GLU: [.][N / 128]
-  int out_dt, act;
+  int out_dt;
   int wide;                  // every output row starts on a 32-byte boundary
   int* status;
   long long wait_limit;
@@ -123,14 +134,21 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint32_t alo, uint32_t ahi
       : "memory");
 }
 
-// four rows of the map's matrix (box 128 x 1) to 512 consecutive bytes
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int x, int r0,
-                                            int r1, int r2, int r3, uint32_t bar) {
+// a 3-D box: the same rows of consecutive matrices
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z,
+                                            uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // 32 columns of this warp's 32 lanes. The registers are written until the
@@ -278,6 +296,7 @@ template <int MODE, int BN, int LD>
 __device__ __forceinline__ void join_rows(const Params& p, const Unit& t, float* sums, int rank,
                                           bool& over) {
   namespace cg = cooperative_groups;
+  constexpr int ACT = MODE == MODE_GEGLU ? MOE_ACT_GEGLU_TANH : MOE_ACT_SWIGLU;
   cg::cluster_group cluster = cg::this_cluster();
   constexpr int V = BN / 32;               // columns per lane
   const int warp = (threadIdx.x >> 5) - kAccWarp0, lane = threadIdx.x & 31;
@@ -298,11 +317,11 @@ __device__ __forceinline__ void join_rows(const Params& p, const Unit& t, float*
       }
     }
     const size_t row = (size_t)t.r0 + r;
-    if constexpr (MODE == MODE_GLU) {
+    if constexpr (MODE != MODE_STORE) {
       float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = glu(p.act, v[i], v[4 + i]);
+        v[i] = glu(ACT, v[i], v[4 + i]);
         mx = fmaxf(mx, finite_abs(v[i]));
       }
 #pragma unroll
@@ -324,8 +343,9 @@ __device__ __forceinline__ void join_rows(const Params& p, const Unit& t, float*
 
 template <int MODE, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmA,
-                  const __grid_constant__ CUtensorMap tmB) {
+    fp8_tc_kernel(const __grid_constant__ Params p) {
+  constexpr bool GLU = MODE != MODE_STORE;
+  constexpr int ACT = MODE == MODE_GEGLU ? MOE_ACT_GEGLU_TANH : MOE_ACT_SWIGLU;
   using C = Cfg<BN, SPLIT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -349,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(full + i), GLU ? 3 : 1);    // the TMA warp, the two gatherers
       mbar_init(smem_u32(empty + i), 1);
     }
     for (int i = 0; i < C::NBUF; ++i) {
@@ -360,8 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmB)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -396,54 +415,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- loads (TMA)
       uint32_t it = 0;
       bool ok = true;
+      if (lane == 0) {
+        for (int u = u0; u < total && ok; u += u_step) {
+          const Unit t = decode(p, s_toff, s_roff, u);
+          const int wrow = t.e * p.rows_per_group + t.unit * BN;
+          // a last unit of at most 128 columns loads that many weight rows (the
+          // rest of the stage keeps old codes, whose columns are not stored)
+          const bool narrow = !GLU && BN > kBlock && p.N - t.unit * BN <= kBlock;
+          const int am = t.nv <= a_rows(0) ? 0 : t.nv <= a_rows(1) ? 1 : 2;
+          const uint32_t bytes = (GLU ? 0u : (uint32_t)(a_rows(am) * kBlock)) +
+                                 (narrow ? (uint32_t)(kBlock * kBlock) : (uint32_t)C::B_BYTES);
+          for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+            const uint32_t s = it % C::NS;
+            if (it >= (uint32_t)C::NS) {
+              ok = mbar_wait(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
+                             true, p.wait_limit);
+              if (!ok) break;
+            }
+            const uint32_t dst = st_base + s * C::STAGE;
+            const uint32_t bar = smem_u32(full + s);
+            const int x = kb * kBlock;
+            mbar_arrive_tx(bar, bytes);
+            if constexpr (GLU) {
+              tma_load_3d(dst + A_BYTES, &p.tmB, x, t.unit * kBlock, 2 * t.e, bar);
+            } else {
+              tma_load_2d(dst + A_BYTES, narrow ? &p.tmB1 : &p.tmB, x, wrow, bar);
+              tma_load_2d(dst, &p.tmA[am], x, t.r0, bar);
+            }
+          }
+        }
+      for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
+        const uint32_t last = it - 1 - i;
+          mbar_wait(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status, false);
+        }
+      }
+      __syncwarp();
+    } else if (GLU && warp >= 2) {
+      // ---------------------------------------------------------- token rows
+      // thread: 16-byte chunk `ch` of rows row0, row0 + 8, ...; chunk c of row r
+      // lies at 16 (c ^ r % 8) within its row
+      const int tid = threadIdx.x - 2 * 32;
+      const int ch = tid & 7, row0 = tid >> 3;
+      constexpr int RSTEP = kGatherThreads / 8, NR = BM / RSTEP;
+      const uint32_t dst0 = st_base + row0 * kBlock + ((ch ^ row0) << 4);
+      uint32_t it = 0;
+      bool ok = true;
+      auto arrive = [&](uint32_t i) {          // this warp's copies of k-block i have landed
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(full + i % C::NS));
+      };
       for (int u = u0; u < total && ok; u += u_step) {
         const Unit t = decode(p, s_toff, s_roff, u);
-        const int wrow = t.e * p.rows_per_group + t.unit * (MODE == MODE_GLU ? kBlock : BN);
-        // boxes of weight rows that the product has (the rest of the stage
-        // keeps old codes, whose columns are not stored)
-        const int boxes = MODE == MODE_GLU ? 2 : min(BN, p.N - t.unit * BN) > kBlock ? 2 : 1;
-        constexpr int BOX_BYTES = kBlock * kBlock;
-        const int up = MODE == MODE_GLU ? p.N : kBlock;       // second box's row offset
-        int rows[4] = {0, 0, 0, 0};
-        int a_bytes;
-        if (p.row_map) {
-          a_bytes = (t.nv + 3) / 4 * 512;
-          if (4 * lane < t.nv) {
+        uint32_t rows[NR];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              rows[i] = (int)__ldg(p.row_map + t.r0 + min(4 * lane + i, t.nv - 1));
-          }
-        } else {
-          a_bytes = (t.nv + A_BOX - 1) / A_BOX * (A_BOX * kBlock);
-        }
-        for (int kb = kb_lo; kb < kb_hi && ok; ++kb, ++it) {
+        for (int i = 0; i < NR; ++i)
+          rows[i] = row0 + i * RSTEP < t.nv ? __ldg(p.row_map + t.r0 + row0 + i * RSTEP) : 0u;
+        for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
           const uint32_t s = it % C::NS;
           if (it >= (uint32_t)C::NS) {
             ok = mbar_wait_warp(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
                                 true, p.wait_limit);
             if (!ok) break;
           }
-          const uint32_t dst = st_base + s * C::STAGE;
-          const uint32_t bar = smem_u32(full + s);
-          const int x = kb * kBlock;
-          if (lane == 0) {
-            mbar_arrive_tx(bar, (uint32_t)(a_bytes + boxes * BOX_BYTES));
-            tma_load_2d(dst + A_BYTES, &tmB, x, wrow, bar);
-            if (boxes == 2) tma_load_2d(dst + A_BYTES + BOX_BYTES, &tmB, x, wrow + up, bar);
-            if (!p.row_map)
-              for (int r = 0; r < t.nv; r += A_BOX)
-                tma_load_2d(dst + r * kBlock, &tmA, x, t.r0 + r, bar);
+          const uint8_t* src = p.x + kb * kBlock + ch * 16;
+          const uint32_t dst = dst0 + s * C::STAGE;
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            if (row0 + i * RSTEP < t.nv)
+              cp_async16(dst + i * (RSTEP * kBlock), src + (size_t)rows[i] * p.K);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (it >= (uint32_t)kGatherLag) {
+            cp_async_wait<kGatherLag>();
+            arrive(it - kGatherLag);
           }
-          __syncwarp();
-          if (p.row_map && 4 * lane < t.nv)
-            tma_gather4(dst + lane * 512, &tmA, x, rows[0], rows[1], rows[2], rows[3], bar);
         }
       }
-      for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
-        const uint32_t last = it - 1 - i;
-        mbar_wait_warp(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status,
-                       false);
-      }
+      cp_async_wait<0>();
+      for (uint32_t i = it < (uint32_t)kGatherLag ? 0 : it - kGatherLag; i < it; ++i) arrive(i);
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -487,32 +536,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     // the thread's columns: two runs of COLS / 2, one of gate and one of up
     // columns, or one after the other
-    const int c0 = MODE == MODE_GLU ? half * (COLS / 2) : half * COLS;
-    const int c1 = MODE == MODE_GLU ? BN / 2 + c0 : c0 + COLS / 2;
+    const int c0 = MODE != MODE_STORE ? half * (COLS / 2) : half * COLS;
+    const int c1 = MODE != MODE_STORE ? BN / 2 + c0 : c0 + COLS / 2;
     uint32_t it = 0, tiles = 0;
     bool ok = true, over = false;
+    // where a unit's scales are, and their first values: taken for the next
+    // unit before the present one is stored
+    Unit t;
+    const float *sa, *w0, *w1;
+    float a = 0.f, b0 = 0.f, b1 = 0.f;
+    auto begin = [&](int u) {
+      t = decode(p, s_toff, s_roff, u);
+      int xrow = t.r0 + min(q * 32 + lane, t.nv - 1);
+      if (GLU) xrow = (int)__ldg(p.row_map + xrow);
+      sa = p.xs + (size_t)xrow * p.KB;
+      const float* wsc = p.ws + (size_t)t.e * p.scale_rows * p.KB;
+      // the scale rows of the two halves of the columns (columns past N have
+      // none of their own and are not stored)
+      const int n0 = GLU ? t.unit : min((t.unit * BN + c0) / kBlock, p.scale_rows - 1);
+      w0 = wsc + (size_t)n0 * p.KB;
+      w1 = GLU ? w0 + (size_t)(p.N / kBlock) * p.KB : w0;
+      a = __ldg(sa + kb_lo);
+      b0 = __ldg(w0 + kb_lo);
+      b1 = __ldg(w1 + kb_lo);
+    };
+    if (u0 < total) begin(u0);
     for (int u = u0; u < total && ok; u += u_step, ++tiles) {
-      const Unit t = decode(p, s_toff, s_roff, u);
       const bool live = q * 32 < t.nv;            // some of the warp's lanes are rows
       const int m = q * 32 + lane;
-      int xrow = t.r0 + min(m, t.nv - 1);
-      if (p.row_map) xrow = (int)__ldg(p.row_map + xrow);
-      const float* sa = p.xs + (size_t)xrow * p.KB;
-      const float* wsc = p.ws + (size_t)t.e * p.scale_rows * p.KB;
-      int n0, n1;                                 // scale rows of the two runs
-      if (MODE == MODE_GLU) {
-        n0 = t.unit;
-        n1 = p.N / kBlock + t.unit;
-      } else {
-        // a run past N has no scale of its own and is not stored
-        n0 = min((t.unit * BN + c0) / kBlock, p.scale_rows - 1);
-        n1 = min((t.unit * BN + c1) / kBlock, p.scale_rows - 1);
-      }
-      const float *w0 = wsc + (size_t)n0 * p.KB, *w1 = wsc + (size_t)n1 * p.KB;
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      float a = __ldg(sa + kb_lo), b0 = __ldg(w0 + kb_lo), b1 = __ldg(w1 + kb_lo);
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const float f0 = a * b0, f1 = a * b1;
         if (kb + 1 < kb_hi) {                     // the next block's, ahead of the wait
@@ -554,6 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      const Unit done = t;
+      if (!SPLIT && u + u_step < total) begin(u + u_step);
       if constexpr (SPLIT) {
         // every MMA of this CTA is done and every load consumed: the ring is free
         constexpr int H = COLS / 2;
@@ -566,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if constexpr (MODE == MODE_STORE) {
         if (live)
-          store_rows<COLS, C::PATCH_LD>(p, t.r0, q * 32, t.nv, t.unit * BN + c0, acc,
+          store_rows<COLS, C::PATCH_LD>(p, done.r0, q * 32, done.nv, done.unit * BN + c0, acc,
                                         s_patch + (warp - kAccWarp0) * 32 * C::PATCH_LD, over);
       } else {
         constexpr int H = COLS / 2;
@@ -574,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
 #pragma unroll
           for (int j = 0; j < H; ++j) {
-            acc[j] = glu(p.act, acc[j], acc[H + j]);
+            acc[j] = glu(ACT, acc[j], acc[H + j]);
             mx = fmaxf(mx, finite_abs(acc[j]));
           }
         }
@@ -587,11 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(xchg));
         ok = mbar_wait_warp(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
         if (!ok) break;
-        if (m < t.nv) {
+        if (m < done.nv) {
           mx = fmaxf(am[m], am[BM + m]);
           const float r = rscale_of(mx);
-          uint8_t* o = reinterpret_cast<uint8_t*>(p.out) + ((size_t)t.r0 + m) * p.N +
-                       t.unit * kBlock + c0;
+          uint8_t* o = reinterpret_cast<uint8_t*>(p.out) + ((size_t)done.r0 + m) * p.N +
+                       done.unit * kBlock + c0;
 #pragma unroll
           for (int j = 0; j < H; j += 32) {
             uint32_t v[8];
@@ -607,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (half == 0)
-            p.out_s[((size_t)t.r0 + m) * (p.N / kBlock) + t.unit] = scale_of(mx);
+            p.out_s[((size_t)done.r0 + m) * (p.N / kBlock) + done.unit] = scale_of(mx);
         }
       }
     }
@@ -633,8 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host
 
 template <int MODE, int BN, bool SPLIT>
-static cudaError_t launch(const Params& p, const CUtensorMap& ta, const CUtensorMap& tb,
-                          unsigned grid, cudaStream_t s) {
+static cudaError_t launch(const Params& p, unsigned grid, cudaStream_t s) {
   auto kern = fp8_tc_kernel<MODE, BN, SPLIT>;
   constexpr int smem = Cfg<BN, SPLIT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -653,8 +708,27 @@ static cudaError_t launch(const Params& p, const CUtensorMap& ta, const CUtensor
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, p, ta, tb);
+  e = cudaLaunchKernelEx(&cfg, kern, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// [2 E][F][K] weight codes: boxes of 128 codes x 128 rows of a gate block and
+// the same rows of its up block
+static bool gate_up_map(CUtensorMap* m, const void* w, int E, int F, int K) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)F, 2 * (cuuint64_t)E};
+  cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)F * K};
+  cuuint32_t box[3] = {kBlock, kBlock, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static bool row_map2d(CUtensorMap* m, const void* base, long long rows, int K, int box_rows) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, K, (uint64_t)rows, K, kBlock, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // tiles: token tiles at most. The split form is taken where the persistent
@@ -663,32 +737,41 @@ static cudaError_t launch(const Params& p, const CUtensorMap& ta, const CUtensor
 template <int MODE>
 static cudaError_t run(Params& p, const void* x, long long x_rows, const void* w, long long tiles,
                        cudaStream_t s) {
-  constexpr int BNS = MODE == MODE_GLU ? 256 : 128;          // columns of the split form
+  constexpr bool GLU = MODE != MODE_STORE;
+  constexpr int BNS = GLU ? 256 : 128;                       // columns of the split form
   p.wait_limit = wait_cycles();
-  const int esize = MODE == MODE_GLU ? 1 : p.out_dt == MOE_F32 ? 4 : 2;
+  const int esize = GLU ? 1 : p.out_dt == MOE_F32 ? 4 : 2;
   p.wide = (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) && ((long long)p.N * esize) % 32 == 0;
   // rows are addressed by 32-bit coordinates
   if ((long long)p.E * p.rows_per_group > 0x7fffffffLL) return cudaErrorNotSupported;
-  CUtensorMap ta, tb;
-  if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, p.K, (uint64_t)x_rows, p.K, kBlock,
-                p.row_map ? 1 : A_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.K, (uint64_t)p.E * p.rows_per_group, p.K,
-                kBlock, kBlock, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
   const int sms = num_sms();
-  const int per_tile = MODE == MODE_GLU ? p.N / kBlock : (p.N + 255) / 256;
-  if (tiles * per_tile * 2 > sms) {
+  const int per_tile = GLU ? p.N / kBlock : (p.N + 255) / 256;
+  const bool split = tiles * per_tile * 2 <= sms;
+  const long long w_rows = (long long)p.E * p.rows_per_group;
+  p.x = (const uint8_t*)x;
+  if (GLU) {
+    if (!gate_up_map(&p.tmB, w, p.E, p.N, p.K)) return cudaErrorInvalidValue;
+  } else {
+    if (!row_map2d(&p.tmB1, w, w_rows, p.K, kBlock)) return cudaErrorInvalidValue;
+    if (split)
+      p.tmB = p.tmB1;
+    else if (!row_map2d(&p.tmB, w, w_rows, p.K, 256))
+      return cudaErrorInvalidValue;
+    for (int i = 0; i < A_MAPS; ++i)
+      if (!row_map2d(&p.tmA[i], x, x_rows, p.K, a_rows(i))) return cudaErrorInvalidValue;
+  }
+  if (!split) {
     p.n_units = per_tile;
     p.split = 1;
     const long long units = tiles * per_tile;
     if (units > 0x7fffffffLL) return cudaErrorNotSupported;
-    return launch<MODE, 256, false>(p, ta, tb, units < sms ? (unsigned)units : (unsigned)sms, s);
+    return launch<MODE, 256, false>(p, units < sms ? (unsigned)units : (unsigned)sms, s);
   }
-  p.n_units = MODE == MODE_GLU ? p.N / kBlock : (p.N + BNS - 1) / BNS;
+  p.n_units = GLU ? p.N / kBlock : (p.N + BNS - 1) / BNS;
   const long long units = tiles * p.n_units;
   p.split = 1;
   while (p.split < 8 && units * p.split * 2 <= sms && p.KB >= p.split * 8) p.split *= 2;
-  return launch<MODE, BNS, true>(p, ta, tb, (unsigned)(units * p.split), s);
+  return launch<MODE, BNS, true>(p, (unsigned)(units * p.split), s);
 }
 
 }  // namespace fp8tc
@@ -733,9 +816,10 @@ cudaError_t launch_swiglu_fp8_tc(const void* xq, const float* xs, int T, const u
   p.scale_rows = 2 * ex.F / kBlock;
   p.out = hq;
   p.out_s = hs;
-  p.act = ex.act;
   p.status = status;
-  return run<MODE_GLU>(p, xq, T, ex.w_gu, max_tiles(R, ex.E, BM), s);
+  const long long tiles = max_tiles(R, ex.E, BM);
+  if (ex.act == MOE_ACT_GEGLU_TANH) return run<MODE_GEGLU>(p, xq, T, ex.w_gu, tiles, s);
+  return run<MODE_SWIGLU>(p, xq, T, ex.w_gu, tiles, s);
 }
 
 cudaError_t launch_down_fp8_tc(const void* hq, const float* hs, const int32_t* row_off,
