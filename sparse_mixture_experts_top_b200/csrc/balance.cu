@@ -8,14 +8,17 @@
 //   dL/dlogits[t][e] = dloss coef/B E/(k n_b^2) p_t[e] (c[b][e] - sum_e' c[b][e'] p_t[e'])
 // (the counts are constants of the gradient).
 //
-// One warp takes a token: its row stays in registers between the maximum, the
-// sum and their use, so each pass reads the logits once, and HBM bounds both.
+// LPR lanes take a token (fewer than a warp where the row has fewer than 128
+// experts): its row stays in registers between the maximum, the sum and their
+// use, so each pass reads the logits once, and HBM bounds both. A lane group
+// loads the rows of up to four tokens before it looks at the first, since a
+// single row's chain (load, maximum, exponentials, sum) is all latency.
 // The forward pass adds a CTA's tokens in registers and shared memory, writes
 // one partial row per (chunk of tokens, sequence) pair, and a second kernel
 // adds those in order: no floating-point atomics, so the same inputs give the
 // same bits. A sequence's chunks are consecutive, so the pair (chunk c,
 // sequence b) can own slot c + b: walking the tokens, each new pair raises c,
-// b or both.
+// b or both. One chunk and one sequence need no second kernel.
 #include "common.cuh"
 #include "launch.h"
 
@@ -24,59 +27,108 @@ namespace bal {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-// chunks of tokens at most: three CTAs for each of 148 SMs
-constexpr int kMaxChunks = 444;
-constexpr int kMinChunk = 16;          // tokens per chunk at least (two per warp)
+constexpr int kMaxChunks = 592;        // chunks of tokens at most: four CTAs for each of 148 SMs
+constexpr int kFinishWarps = 32;
 
-static int chunk_of(int T) {
-  const int c = (int)(((long long)T + kMaxChunks - 1) / kMaxChunks);
-  return c < kMinChunk ? kMinChunk : c;
+// How a row of E logits lies in a lane group: LPR lanes, NV steps of VEC
+// consecutive logits each (VEC 4 where every row starts on a 16-byte
+// boundary, E % 4 == 0): lane l holds elements (i LPR + l) VEC + j.
+template <int LPR_, int NV_, int VEC_> struct Shape {
+  static constexpr int LPR = LPR_, NV = NV_, VEC = VEC_, N = NV * VEC;
+  static constexpr int TPW = 32 / LPR;                           // tokens of a warp at a time
+  static constexpr int UN = N <= 8 ? 4 : N <= 16 ? 2 : 1;        // rows in flight per group
+};
+
+// f(Shape) for rows of E logits
+template <typename F> static auto by_width(int E, F&& f) {
+  if (E % 4 == 0) {
+    if (E <= 8) return f(Shape<2, 1, 4>());
+    if (E <= 16) return f(Shape<4, 1, 4>());
+    if (E <= 32) return f(Shape<8, 1, 4>());
+    if (E <= 64) return f(Shape<16, 1, 4>());
+    if (E <= 128) return f(Shape<32, 1, 4>());
+    if (E <= 256) return f(Shape<32, 2, 4>());
+    if (E <= 512) return f(Shape<32, 4, 4>());
+    return f(Shape<32, 8, 4>());
+  }
+  if (E <= 8) return f(Shape<8, 1, 1>());
+  if (E <= 32) return f(Shape<32, 1, 1>());
+  if (E <= 64) return f(Shape<32, 2, 1>());
+  if (E <= 128) return f(Shape<32, 4, 1>());
+  if (E <= 256) return f(Shape<32, 8, 1>());
+  if (E <= 512) return f(Shape<32, 16, 1>());
+  return f(Shape<32, 32, 1>());
 }
-static int chunks_of(int T) { return (int)(((long long)T + chunk_of(T) - 1) / chunk_of(T)); }
 
-// VEC consecutive logits per lane and step, NV steps: element
-// (i * 32 + lane) * VEC + j of the row is v[i * VEC + j]
-template <int NV, int VEC>
+// Tokens per chunk: as many as four CTAs per SM take, at least what a CTA has
+// in flight at a time
+static int chunk_of(int T, int E) {
+  const int least = by_width(E, [](auto s) { return kWarps * decltype(s)::TPW * decltype(s)::UN; });
+  const int c = (int)(((long long)T + kMaxChunks - 1) / kMaxChunks);
+  return c < least ? least : c;
+}
+static int chunks_of(int T, int E) {
+  const int c = chunk_of(T, E);
+  return (int)(((long long)T + c - 1) / c);
+}
+
+template <typename S>
 struct Row {
-  float v[NV * VEC];
+  float v[S::N];
+
+  // element index of value i * VEC + j
+  static __device__ __forceinline__ int at(int i, int j) {
+    return (i * S::LPR + (int)(threadIdx.x % S::LPR)) * S::VEC + j;
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < S::N; ++i) v[i] = -INFINITY;
+  }
 
   __device__ __forceinline__ void load(const float* p, int E) {
-    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = (i * 32 + lane) * VEC;
-      if constexpr (VEC == 4) {
-        uint4 a = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-        if (e < E) a = ldg_nc_v4(p + e);
-        v[4 * i] = __uint_as_float(a.x);
-        v[4 * i + 1] = __uint_as_float(a.y);
-        v[4 * i + 2] = __uint_as_float(a.z);
-        v[4 * i + 3] = __uint_as_float(a.w);
+    for (int i = 0; i < S::NV; ++i) {
+      const int e = at(i, 0);
+      if constexpr (S::VEC == 4) {
+        if (e < E) {
+          const uint4 a = ldg_nc_v4(p + e);
+          v[4 * i] = __uint_as_float(a.x);
+          v[4 * i + 1] = __uint_as_float(a.y);
+          v[4 * i + 2] = __uint_as_float(a.z);
+          v[4 * i + 3] = __uint_as_float(a.w);
+        }
       } else {
-        v[i] = e < E ? __ldg(p + e) : -INFINITY;
+        if (e < E) v[i] = __ldg(p + e);
       }
     }
   }
 
-  // the row's softmax in place; a row of nothing but -inf gives zeros
-  __device__ __forceinline__ void softmax() {
+  // The row's exponentials in place (their largest is 1), and the factor that
+  // makes them probabilities; a row of nothing but -inf gives zeros.
+  // exp(x) = 2^(x log2 e), results below 2^-126 taken as zero.
+  __device__ __forceinline__ float softmax() {
     float m = v[0];
 #pragma unroll
-    for (int i = 1; i < NV * VEC; ++i) m = fmaxf(m, v[i]);
+    for (int i = 1; i < S::N; ++i) m = fmaxf(m, v[i]);
+    if constexpr (S::LPR == 32) {
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // fmaxf passes over NaN: a row of NaN and -inf alone keeps its NaN below
+      for (int o = S::LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    // (the maximum passes over NaN, so a row of NaN and -inf alone has m = -inf
+    // too; its NaN shows in the exponentials)
     float z = 0.f;
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int i = 0; i < NV * VEC; ++i) {
-      v[i] = __expf(v[i] - base);
+    for (int i = 0; i < S::N; ++i) {
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((v[i] - base) * 1.4426950408889634f));
       z += v[i];
     }
-    z = warp_sum(z);
-    const float r = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
-    for (int i = 0; i < NV * VEC; ++i) v[i] *= r;
+    for (int o = S::LPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    return z == 0.f ? 0.f : 1.f / z;
   }
 };
 
@@ -111,90 +163,176 @@ struct FwdParams {
   const uint8_t* mask;
   const int32_t* off;
   int T, E, k, n_seq, chunk, n_chunks;
+  float factor;        // coef E / (n_seq k)
   float* part_p;       // [n_chunks + n_seq][E]
   int32_t* part_c;     // [n_chunks + n_seq][E]
   int32_t* part_n;     // [n_chunks + n_seq]
   float* part_loss;    // [n_seq * ceil(E / 32)]
   unsigned* counter;
+  float* loss;
+  int32_t* counts;
+  float* probs;
+  int32_t* tokens;
 };
 
-template <int NV, int VEC>
+// The sum over a CTA of one value per thread, in a fixed order (thread 0 has it)
+template <int WARPS>
+__device__ __forceinline__ float block_sum(float v, float* s_part) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < WARPS; ++w) v += s_part[w];
+  return v;
+}
+
+// One chunk of tokens: a partial row for each sequence that it meets. SINGLE:
+// the only chunk of the only sequence, whose sums are the result.
+template <typename S, bool SINGLE>
 __global__ void __launch_bounds__(kThreads) partial_kernel(const FwdParams p) {
   extern __shared__ float sm[];
   float* s_p = sm;                                             // [kWarps][E]
   int* s_c = reinterpret_cast<int*>(sm + (size_t)kWarps * p.E);  // [E]
   __shared__ int s_n[kWarps];
+  __shared__ float s_l[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane / S::LPR, gl = lane % S::LPR;
+  constexpr int STEP = kWarps * S::TPW;
   pdl_wait();
   pdl_launch();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;     // for the kernel behind this one
+  if (!SINGLE && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;   // for the next kernel
   const int t1 = (int)min((long long)p.T, (blockIdx.x + 1LL) * p.chunk);
-  for (int t0 = blockIdx.x * p.chunk; t0 < t1;) {
-    int end;
-    const int b = seq_of(p.off, p.n_seq, p.T, t0, end);
-    end = min(max(end, t0 + 1), t1);
-    if (b < 0) {
-      t0 = end;
-      continue;
+  for (int t0 = blockIdx.x * p.chunk; t0 < t1 || SINGLE;) {
+    int end = t1, b = 0;
+    if (t0 < t1) {
+      b = seq_of(p.off, p.n_seq, p.T, t0, end);
+      end = min(max(end, t0 + 1), t1);
+      if (b < 0) {
+        t0 = end;
+        continue;
+      }
     }
     for (int e = threadIdx.x; e < p.E; e += kThreads) s_c[e] = 0;
     __syncthreads();
-    float acc[NV * VEC];
+    float acc[S::N];
 #pragma unroll
-    for (int i = 0; i < NV * VEC; ++i) acc[i] = 0.f;
+    for (int i = 0; i < S::N; ++i) acc[i] = 0.f;
     int n = 0;
-    for (int t = t0 + warp; t < end; t += kWarps) {
-      if (p.mask && !__ldg(p.mask + t)) continue;
-      Row<NV, VEC> r;
-      r.load(p.logits + (size_t)t * p.E, p.E);
-      if (lane < p.k) {
-        const int e = __ldg(p.idx + (size_t)t * p.k + lane);
-        if (e >= 0 && e < p.E) atomicAdd(&s_c[e], 1);          // integers: any order
-      }
-      r.softmax();
+    // The warp's tokens, UF per group and step (the same number of steps in all
+    // its groups): while a step's rows are worked on, the next step's rows and
+    // ids and the masks of the one behind it are on their way.
+    constexpr int UF = S::UN > 1 ? S::UN / 2 : 1;
+    struct Step {
+      Row<S> r[UF];
+      int id[UF];
+      bool ok[UF];
+    } cur, next;
+    bool ok[UF];
+    auto masks = [&](int tw) {
 #pragma unroll
-      for (int i = 0; i < NV * VEC; ++i) acc[i] += r.v[i];
-      ++n;
+      for (int u = 0; u < UF; ++u) {
+        const int t = tw + u * STEP + grp;
+        ok[u] = t < end && (!p.mask || __ldg(p.mask + t));
+      }
+    };
+    auto rows = [&](int tw, Step& s) {
+#pragma unroll
+      for (int u = 0; u < UF; ++u) {
+        const int t = tw + u * STEP + grp;
+        s.ok[u] = ok[u];
+        s.r[u].clear();                   // a token that takes no part has no probability
+        if (ok[u]) s.r[u].load(p.logits + (size_t)t * p.E, p.E);
+        s.id[u] = ok[u] && gl < p.k ? __ldg(p.idx + (size_t)t * p.k + gl) : -1;
+      }
+    };
+    int tw = t0 + warp * S::TPW;
+    if (tw < end) {
+      masks(tw);
+      rows(tw, cur);
+      masks(tw + STEP * UF);
+    }
+    for (; tw < end; tw += STEP * UF) {
+      rows(tw + STEP * UF, next);
+      masks(tw + 2 * STEP * UF);
+#pragma unroll
+      for (int u = 0; u < UF; ++u) {
+        const int e0 = cur.id[u];
+        if (e0 >= 0 && e0 < p.E) atomicAdd(&s_c[e0], 1);       // integers: any order
+        if (cur.ok[u] && gl == 0) ++n;
+        if (S::LPR < 32 && cur.ok[u]) {   // the slots past one per lane
+          const int32_t* ids = p.idx + (size_t)(tw + u * STEP + grp) * p.k;
+          for (int j = gl + S::LPR; j < p.k; j += S::LPR) {
+            const int e = __ldg(ids + j);
+            if (e >= 0 && e < p.E) atomicAdd(&s_c[e], 1);
+          }
+        }
+        __syncwarp();
+        const float f = cur.r[u].softmax();
+#pragma unroll
+        for (int i = 0; i < S::N; ++i) acc[i] = fmaf(cur.r[u].v[i], f, acc[i]);
+      }
+      cur = next;
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int o = S::LPR; o < 32; o <<= 1) {                    // the warp's groups
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int e = (i * 32 + lane) * VEC + j;
-        if (e < p.E) s_p[warp * p.E + e] = acc[i * VEC + j];
-      }
+      for (int i = 0; i < S::N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (grp == 0) {
+#pragma unroll
+      for (int i = 0; i < S::NV; ++i)
+#pragma unroll
+        for (int j = 0; j < S::VEC; ++j) {
+          const int e = Row<S>::at(i, j);
+          if (e < p.E) s_p[warp * p.E + e] = acc[i * S::VEC + j];
+        }
+    }
     if (lane == 0) s_n[warp] = n;
     __syncthreads();
-    const size_t slot = (size_t)blockIdx.x + b;
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n += s_n[w];
+    const size_t slot = SINGLE ? 0 : (size_t)blockIdx.x + b;
+    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+    float l = 0.f;
     for (int e = threadIdx.x; e < p.E; e += kThreads) {
       float v = s_p[e];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) v += s_p[w * p.E + e];
-      p.part_p[slot * p.E + e] = v;
-      p.part_c[slot * p.E + e] = s_c[e];
+      if constexpr (SINGLE) {
+        p.probs[e] = v * inv;
+        p.counts[e] = s_c[e];
+        l += (float)s_c[e] * inv * (v * inv);
+      } else {
+        p.part_p[slot * p.E + e] = v;
+        p.part_c[slot * p.E + e] = s_c[e];
+      }
     }
-    if (threadIdx.x == 0) {
-      int s = 0;
-      for (int w = 0; w < kWarps; ++w) s += s_n[w];
-      p.part_n[slot] = s;
+    if constexpr (SINGLE) {
+      l = block_sum<kWarps>(l, s_l);
+      if (threadIdx.x == 0) {
+        *p.loss = p.factor * l;
+        p.tokens[0] = n;
+      }
+      return;
     }
+    if (threadIdx.x == 0) p.part_n[slot] = n;
     __syncthreads();
     t0 = end;
   }
 }
 
-// 32 experts of one sequence per CTA: the 8 warps add every 8th chunk's
-// partial sums, then those eight in order. The last CTA to finish adds the
-// CTAs' parts of the loss, in order.
-__global__ void __launch_bounds__(kThreads) finish_kernel(const FwdParams p, float coef,
-                                                          float* __restrict__ loss,
-                                                          int32_t* __restrict__ counts,
-                                                          float* __restrict__ probs,
-                                                          int32_t* __restrict__ tokens) {
-  __shared__ float s_p[kWarps][32];
-  __shared__ int s_c[kWarps][32];
-  __shared__ int s_n[kWarps];
-  __shared__ float s_l[kWarps];
+// 32 experts of one sequence per CTA: the warps add every 32nd chunk's partial
+// sums, then those in order. The last CTA to finish adds the CTAs' parts of
+// the loss, in order.
+__global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const FwdParams p) {
+  __shared__ float s_p[kFinishWarps][32];
+  __shared__ int s_c[kFinishWarps][32];
+  __shared__ int s_n[kFinishWarps];
+  __shared__ float s_l[kFinishWarps];
   __shared__ bool s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -210,8 +348,8 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const FwdParams p, flo
   int c = 0, n = 0;
   if (t0 < t1) {
     const int c1 = (t1 - 1) / p.chunk;
-#pragma unroll 4
-    for (int i = t0 / p.chunk + warp; i <= c1; i += kWarps) {
+#pragma unroll 8
+    for (int i = t0 / p.chunk + warp; i <= c1; i += kFinishWarps) {
       const size_t slot = (size_t)i + b;
       if (e < p.E) {
         v += p.part_p[slot * p.E + e];
@@ -228,7 +366,8 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const FwdParams p, flo
     v = 0.f;
     c = 0;
     n = 0;
-    for (int w = 0; w < kWarps; ++w) {
+#pragma unroll
+    for (int w = 0; w < kFinishWarps; ++w) {
       v += s_p[w][lane];
       c += s_c[w][lane];
       n += s_n[w];
@@ -236,14 +375,14 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const FwdParams p, flo
     const float inv = n > 0 ? 1.f / (float)n : 0.f;
     v *= inv;
     if (e < p.E) {
-      counts[(size_t)b * p.E + e] = c;
-      probs[(size_t)b * p.E + e] = v;
+      p.counts[(size_t)b * p.E + e] = c;
+      p.probs[(size_t)b * p.E + e] = v;
     } else {
       v = 0.f;
     }
     const float l = warp_sum((float)c * inv * v);
     if (lane == 0) {
-      if (blockIdx.x % eb == 0) tokens[b] = n;
+      if (blockIdx.x % eb == 0) p.tokens[b] = n;
       p.part_loss[blockIdx.x] = l;
       __threadfence();
       s_last = atomicAdd(p.counter, 1u) == gridDim.x - 1;
@@ -253,15 +392,10 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const FwdParams p, flo
   if (!s_last) return;
   __threadfence();
   float l = 0.f;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) l += __ldcg(p.part_loss + i);
-  l = warp_sum(l);
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    l = 0.f;
-    for (int w = 0; w < kWarps; ++w) l += s_l[w];
-    *loss = coef * ((float)p.E / ((float)p.n_seq * (float)p.k)) * l;
-  }
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinishWarps * 32)
+    l += __ldcg(p.part_loss + i);
+  l = block_sum<kFinishWarps>(l, s_l);
+  if (threadIdx.x == 0) *p.loss = p.factor * l;
 }
 
 struct BwdParams {
@@ -276,59 +410,73 @@ struct BwdParams {
   float* dlogits;
 };
 
-// A warp takes `chunk` consecutive tokens; the counts of their sequence stay
-// in registers.
-template <int NV, int VEC>
+// A warp takes `chunk` consecutive tokens; the counts of a group's sequence
+// stay in registers.
+template <typename S>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane / S::LPR;
   pdl_wait();
   pdl_launch();
   const long long first = ((long long)blockIdx.x * kWarps + warp) * p.chunk;
   const int t1 = (int)min((long long)p.T, first + p.chunk);
   const float up = p.dloss ? __ldg(p.dloss) : 1.f;
   int b = -1, end = 0;
-  float a[NV * VEC];
+  float a[S::N];
 #pragma unroll
-  for (int i = 0; i < NV * VEC; ++i) a[i] = 0.f;
-  for (int t = (int)min((long long)p.T, first); t < t1; ++t) {
-    if (t >= end) {
-      b = seq_of(p.off, p.n_seq, p.T, t, end);
-      if (b >= 0) {
-        const float n = (float)max(__ldg(p.tokens + b), 1);
+  for (int i = 0; i < S::N; ++i) a[i] = 0.f;
+  for (int tw = (int)min((long long)p.T, first); tw < t1; tw += S::TPW * S::UN) {
+    Row<S> r[S::UN];
+    bool ok[S::UN];
+#pragma unroll
+    for (int u = 0; u < S::UN; ++u) {
+      const int t = tw + u * S::TPW + grp;
+      ok[u] = t < t1 && (!p.mask || __ldg(p.mask + t));
+    }
+#pragma unroll
+    for (int u = 0; u < S::UN; ++u) {
+      r[u].clear();
+      if (ok[u]) r[u].load(p.logits + (size_t)(tw + u * S::TPW + grp) * p.E, p.E);
+    }
+#pragma unroll
+    for (int u = 0; u < S::UN; ++u) {
+      const int t = tw + u * S::TPW + grp;
+      if (t < t1 && t >= end) {
+        b = seq_of(p.off, p.n_seq, p.T, t, end);
+        const float n = b >= 0 ? (float)max(__ldg(p.tokens + b), 1) : 1.f;
         const float f = up * p.factor / (n * n);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < S::NV; ++i)
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const int e = (i * 32 + lane) * VEC + j;
-            a[i * VEC + j] = e < p.E ? f * (float)__ldg(p.counts + (size_t)b * p.E + e) : 0.f;
+          for (int j = 0; j < S::VEC; ++j) {
+            const int e = Row<S>::at(i, j);
+            a[i * S::VEC + j] =
+                b >= 0 && e < p.E ? f * (float)__ldg(p.counts + (size_t)b * p.E + e) : 0.f;
           }
       }
-    }
-    float* out = p.dlogits + (size_t)t * p.E;
-    Row<NV, VEC> r;
-    if (b >= 0 && (!p.mask || __ldg(p.mask + t))) {
-      r.load(p.logits + (size_t)t * p.E, p.E);
-      r.softmax();
+      __syncwarp();
+      const float z = r[u].softmax();    // zeros for a masked token
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV * VEC; ++i) s = fmaf(a[i], r.v[i], s);
-      s = warp_sum(s);
+      for (int i = 0; i < S::N; ++i) s = fmaf(a[i], r[u].v[i], s);
 #pragma unroll
-      for (int i = 0; i < NV * VEC; ++i) r.v[i] *= a[i] - s;
-    } else {
+      for (int o = S::LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s *= z;
+      if (t >= t1) continue;
+      float* out = p.dlogits + (size_t)t * p.E;
 #pragma unroll
-      for (int i = 0; i < NV * VEC; ++i) r.v[i] = 0.f;
-    }
+      for (int i = 0; i < S::NV; ++i) {
+        const int e = Row<S>::at(i, 0);
+        if (e >= p.E) continue;
+        float d[S::VEC];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = (i * 32 + lane) * VEC;
-      if (e < p.E) {
-        if constexpr (VEC == 4)
-          *reinterpret_cast<float4*>(out + e) =
-              make_float4(r.v[4 * i], r.v[4 * i + 1], r.v[4 * i + 2], r.v[4 * i + 3]);
+        for (int j = 0; j < S::VEC; ++j)
+          // (a token of no sequence is zero whatever its logits hold)
+          d[j] = b >= 0 ? r[u].v[i * S::VEC + j] * z * (a[i * S::VEC + j] - s) : 0.f;
+        if constexpr (S::VEC == 4)
+          *reinterpret_cast<float4*>(out + e) = make_float4(d[0], d[1], d[2], d[3]);
         else
-          out[e] = r.v[i];
+          out[e] = d[0];
       }
     }
   }
@@ -339,7 +487,7 @@ struct Ws {
 };
 static Ws layout(int T, int E, int n_seq) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-  const size_t slots = (size_t)chunks_of(T) + n_seq;
+  const size_t slots = (size_t)chunks_of(T, E) + n_seq;
   Ws w;
   w.p = 0;
   w.c = up(slots * E * 4);
@@ -349,42 +497,6 @@ static Ws layout(int T, int E, int n_seq) {
   w.total = w.counter + 256;
   return w;
 }
-
-// f<NV, VEC>() for rows of E logits: 16-byte loads where every row starts on
-// a 16-byte boundary (E % 4 == 0)
-template <template <int, int> class F, typename P>
-static cudaError_t by_width(int E, const P& a) {
-  if (E % 4 == 0) {
-    if (E <= 128) return F<1, 4>::run(a);
-    if (E <= 256) return F<2, 4>::run(a);
-    if (E <= 512) return F<4, 4>::run(a);
-    return F<8, 4>::run(a);
-  }
-  if (E <= 32) return F<1, 1>::run(a);
-  if (E <= 64) return F<2, 1>::run(a);
-  if (E <= 128) return F<4, 1>::run(a);
-  if (E <= 256) return F<8, 1>::run(a);
-  if (E <= 512) return F<16, 1>::run(a);
-  return F<32, 1>::run(a);
-}
-
-template <typename P> struct Launch {
-  P p;
-  unsigned grid;
-  cudaStream_t s;
-};
-template <int NV, int VEC> struct RunFwd {
-  static cudaError_t run(const Launch<FwdParams>& l) {
-    launch_pdl(partial_kernel<NV, VEC>, l.grid, kThreads, (size_t)(kWarps + 1) * l.p.E * 4, l.s, l.p);
-    return cudaGetLastError();
-  }
-};
-template <int NV, int VEC> struct RunBwd {
-  static cudaError_t run(const Launch<BwdParams>& l) {
-    launch_pdl(backward_kernel<NV, VEC>, l.grid, kThreads, 0, l.s, l.p);
-    return cudaGetLastError();
-  }
-};
 
 }  // namespace bal
 
@@ -397,16 +509,23 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const u
   using namespace bal;
   const Ws w = layout(T, E, n_seq);
   char* base = static_cast<char*>(ws);
-  FwdParams p{logits, idx, mask, seq_off, T, E, k, n_seq, chunk_of(T), chunks_of(T),
-              (float*)(base + w.p), (int32_t*)(base + w.c), (int32_t*)(base + w.n),
-              (float*)(base + w.loss), (unsigned*)(base + w.counter)};
+  const FwdParams p{logits, idx, mask, seq_off, T, E, k, n_seq, chunk_of(T, E), chunks_of(T, E),
+                    coef * ((float)E / ((float)n_seq * (float)k)),
+                    (float*)(base + w.p), (int32_t*)(base + w.c), (int32_t*)(base + w.n),
+                    (float*)(base + w.loss), (unsigned*)(base + w.counter),
+                    loss, counts, probs, tokens};
+  const bool single = p.n_chunks <= 1 && n_seq == 1;
+  const size_t smem = (size_t)(kWarps + 1) * E * 4;
   // at least one CTA, which clears the counter
-  const Launch<FwdParams> l{p, (unsigned)(p.n_chunks > 0 ? p.n_chunks : 1), s};
-  cudaError_t e = by_width<RunFwd>(E, l);
-  if (e != cudaSuccess) return e;
-  launch_pdl(finish_kernel, (unsigned)((E + 31) / 32) * (unsigned)n_seq, kThreads, 0, s, p, coef,
-             loss, counts, probs, tokens);
-  return cudaGetLastError();
+  const unsigned grid = (unsigned)(p.n_chunks > 0 ? p.n_chunks : 1);
+  const cudaError_t e = by_width(E, [&](auto shape) {
+    using S = decltype(shape);
+    if (single) return launch_pdl(partial_kernel<S, true>, 1, kThreads, smem, s, p);
+    return launch_pdl(partial_kernel<S, false>, grid, kThreads, smem, s, p);
+  });
+  if (e != cudaSuccess || single) return e;
+  return launch_pdl(finish_kernel, (unsigned)((E + 31) / 32) * (unsigned)n_seq, kFinishWarps * 32,
+                    0, s, p);
 }
 
 cudaError_t launch_balance_loss_backward(const float* logits, const uint8_t* mask,
@@ -414,13 +533,20 @@ cudaError_t launch_balance_loss_backward(const float* logits, const uint8_t* mas
                                          float coef, const int32_t* counts, const int32_t* tokens,
                                          const float* dloss, float* dlogits, cudaStream_t s) {
   using namespace bal;
-  // consecutive tokens of one warp: as many as leave four CTAs for each SM
-  const int chunk = (int)(((long long)T + 148 * 4 * kWarps - 1) / (148 * 4 * kWarps));
-  BwdParams p{logits, mask, seq_off, counts, tokens, dloss, T, E, n_seq, chunk,
-              coef * ((float)E / ((float)n_seq * (float)k)), dlogits};
-  const long long warps = ((long long)T + chunk - 1) / chunk;
-  const Launch<BwdParams> l{p, (unsigned)((warps + kWarps - 1) / kWarps), s};
-  return by_width<RunBwd>(E, l);
+  return by_width(E, [&](auto shape) {
+    using S = decltype(shape);
+    // consecutive tokens of one warp: as many as leave eight CTAs for each SM,
+    // at least what it has in flight at a time
+    constexpr int kCtas = 148 * 8;
+    const int c = (int)(((long long)T + kCtas * kWarps - 1) / (kCtas * kWarps));
+    const int least = S::TPW * S::UN;
+    const int chunk = c < least ? least : c;
+    const BwdParams p{logits, mask, seq_off, counts, tokens, dloss, T, E, n_seq, chunk,
+                      coef * ((float)E / ((float)n_seq * (float)k)), dlogits};
+    const long long warps = ((long long)T + chunk - 1) / chunk;
+    return launch_pdl(backward_kernel<S>, (unsigned)((warps + kWarps - 1) / kWarps), kThreads, 0, s,
+                      p);
+  });
 }
 
 }  // namespace moe
