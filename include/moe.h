@@ -384,7 +384,8 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
  *   tokens   (device, out) int32 [n_seq]: n_b
  *   ws       (device) scratch of moe_balance_loss_workspace(T, E, n_seq) bytes
  *            (contents on entry do not matter; calls that may overlap on the
- *            GPU need one each)
+ *            GPU need one each; 0 bytes for a few tokens of one sequence: ws
+ *            may be NULL then)
  * Logits of -inf have probability 0; a row of nothing else adds no
  * probability. fp32 sums in a fixed order: the same inputs give the same bits.
  * T = 0 is valid and writes zeros. */

@@ -291,13 +291,16 @@ FP8_BLOCK = 128
 def _on(*ts):
     """Contiguous tensors of the current device, where the launches go; the
     raw handle of its current stream."""
-    dev = torch.cuda.current_device()
+    dev = -1
     for t in ts:
         if t is not None:
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("inputs must be contiguous CUDA tensors")
             if t.get_device() != dev:
-                raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+                if dev >= 0 or t.get_device() != torch.cuda.current_device():
+                    raise ValueError(f"a tensor is on {t.device}, the call is for the current "
+                                     f"device, cuda:{torch.cuda.current_device()}")
+                dev = t.get_device()
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -370,20 +373,26 @@ def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
 def _f8_experts(ex) -> Experts:
     """C view of f8 experts, whose shapes the grouped calls rely on."""
     fmt = ex.fmt
-    if (_FMT[fmt] if isinstance(fmt, str) else int(fmt)) == W_F8:
-        E, d, F, B = ex.E, ex.d, ex.F, FP8_BLOCK
-        if ex.w_gu.shape != (E, 2 * F, d) or ex.w_dn.shape != (E, d, F):
-            raise ValueError("f8 experts: w_gu must be [E, 2F, d] and w_dn [E, d, F]")
-        _is(ex.s_gu, torch.float32, (E, 2 * F // B, d // B), "s_gu")
-        _is(ex.s_dn, torch.float32, (E, d // B, F // B), "s_dn")
-    return experts_struct(ex)
+    if fmt != "f8" and fmt != W_F8:
+        return experts_struct(ex)                    # the library refuses it
+    w_gu, s_gu, w_dn, s_dn, act = ex.w_gu, ex.s_gu, ex.w_dn, ex.s_dn, getattr(ex, "act", "swiglu")
+    E, d, F, B = ex.E, ex.d, ex.F, FP8_BLOCK
+    if w_gu.shape != (E, 2 * F, d) or w_dn.shape != (E, d, F):
+        raise ValueError("f8 experts: w_gu must be [E, 2F, d] and w_dn [E, d, F]")
+    _codes(w_gu, 3, "w_gu")
+    _codes(w_dn, 3, "w_dn")
+    _is(s_gu, torch.float32, (E, 2 * F // B, d // B), "s_gu")
+    _is(s_dn, torch.float32, (E, d // B, F // B), "s_dn")
+    _on(w_gu, s_gu, w_dn, s_dn)
+    return Experts(W_F8, E, d, F, w_gu.data_ptr(), s_gu.data_ptr(), None, w_dn.data_ptr(),
+                   s_dn.data_ptr(), None, _ACT[act] if isinstance(act, str) else int(act))
 
 
 def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUTO, stream=None):
     """-> (hq e4m3 [T*k, F], hs fp32 [T*k, F/128]): gate|up and GLU of f8 experts
     from quantised token rows xq [T, d], xs [T, d/128] (quantize_fp8)."""
     rmap, roff, toff = tables.row_map, tables.row_off, tables.tile_off
-    raw = _on(xq, xs, rmap, roff, toff, experts.w_gu)
+    raw = _on(xq, xs, rmap, roff, toff)
     _codes(xq, 2, "xq")
     T, d = xq.shape
     if d != experts.d:
@@ -407,7 +416,7 @@ def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AU
     """-> ys fp16 [T*k, d] from quantised rows hq [T*k, F], hs [T*k, F/128]
     (grouped_swiglu_fp8)."""
     roff, toff = tables.row_off, tables.tile_off
-    raw = _on(hq, hs, roff, toff, experts.w_dn)
+    raw = _on(hq, hs, roff, toff)
     _codes(hq, 2, "hq")
     R, F = T * k, experts.F
     if hq.shape != (R, F):
@@ -463,13 +472,15 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
     counts = topk_idx.new_empty((B, E))
     tokens = topk_idx.new_empty((B,))
     if ws is None:
-        ws = logits.new_empty((lib.moe_balance_loss_workspace(T, E, B),), dtype=torch.uint8)
-        if stream is not None:
-            ws.record_stream(stream)     # freed here, still in use there
+        need = lib.moe_balance_loss_workspace(T, E, B)
+        if need:
+            ws = logits.new_empty((need,), dtype=torch.uint8)
+            if stream is not None:
+                ws.record_stream(stream)     # freed here, still in use there
     _check(lib.moe_balance_loss(logits.data_ptr(), topk_idx.data_ptr(), _at(mask), _at(seq_off), T,
                                 E, k, B, coef, loss.data_ptr(), counts.data_ptr(),
-                                probs.data_ptr(), tokens.data_ptr(), ws.data_ptr(), ws.nbytes,
-                                raw if stream is None else stream.cuda_stream),
+                                probs.data_ptr(), tokens.data_ptr(), _at(ws),
+                                0 if ws is None else ws.nbytes, raw if stream is None else stream.cuda_stream),
            "moe_balance_loss")
     return BalanceStats(loss, counts, probs, tokens)
 

@@ -431,7 +431,7 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
 static const int kMaxSeqs = 1 << 16;
 
 size_t moe_balance_loss_workspace(int T, int E, int n_seq) {
-  if (T < 0 || E <= 0 || n_seq < 1) return 0;
+  if (T < 0 || E <= 0 || E > 1024 || n_seq < 1) return 0;
   return balance_workspace_bytes(T, E, n_seq);
 }
 
@@ -451,8 +451,8 @@ moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const 
   if (!loss || !counts || !probs || !tokens) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits)) return MOE_ERR_INVALID_ARG;
-  if (!ws || !aligned16(ws) || ws_bytes < moe_balance_loss_workspace(T, E, n_seq))
-    return MOE_ERR_WORKSPACE;
+  const size_t need = moe_balance_loss_workspace(T, E, n_seq);
+  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   return launched(launch_balance_loss(logits, topk_idx, mask, seq_off, T, E, k, n_seq, coef, loss,
                                       counts, probs, tokens, ws, (cudaStream_t)stream));
 }

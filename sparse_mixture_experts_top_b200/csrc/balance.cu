@@ -500,7 +500,12 @@ static Ws layout(int T, int E, int n_seq) {
 
 }  // namespace bal
 
-size_t balance_workspace_bytes(int T, int E, int n_seq) { return bal::layout(T, E, n_seq).total; }
+// one chunk and one sequence: no partial sums
+static bool single(int T, int E, int n_seq) { return n_seq == 1 && bal::chunks_of(T, E) <= 1; }
+
+size_t balance_workspace_bytes(int T, int E, int n_seq) {
+  return single(T, E, n_seq) ? 0 : bal::layout(T, E, n_seq).total;
+}
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask,
                                 const int32_t* seq_off, int T, int E, int k, int n_seq, float coef,
@@ -514,16 +519,16 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const u
                     (float*)(base + w.p), (int32_t*)(base + w.c), (int32_t*)(base + w.n),
                     (float*)(base + w.loss), (unsigned*)(base + w.counter),
                     loss, counts, probs, tokens};
-  const bool single = p.n_chunks <= 1 && n_seq == 1;
+  const bool one = single(T, E, n_seq);
   const size_t smem = (size_t)(kWarps + 1) * E * 4;
   // at least one CTA, which clears the counter
   const unsigned grid = (unsigned)(p.n_chunks > 0 ? p.n_chunks : 1);
   const cudaError_t e = by_width(E, [&](auto shape) {
     using S = decltype(shape);
-    if (single) return launch_pdl(partial_kernel<S, true>, 1, kThreads, smem, s, p);
+    if (one) return launch_pdl(partial_kernel<S, true>, 1, kThreads, smem, s, p);
     return launch_pdl(partial_kernel<S, false>, grid, kThreads, smem, s, p);
   });
-  if (e != cudaSuccess || single) return e;
+  if (e != cudaSuccess || one) return e;
   return launch_pdl(finish_kernel, (unsigned)((E + 31) / 32) * (unsigned)n_seq, kFinishWarps * 32,
                     0, s, p);
 }

@@ -122,10 +122,11 @@ def test_calls_refuse_bad_arguments_without_launching(moe):
     assert f(T=-1) == ARG and f(k=9) == ARG and f(k=0) == ARG and f(E=0) == ARG
     assert f(B=0) == ARG and f(B=2) == ARG            # several sequences without offsets
     assert f(E=2048) == UNS and f(E=64, k=33) == UNS and f(off=p, B=65537) == UNS
-    assert f(ws=P) == moe.ERR_WORKSPACE and f(n=8) == moe.ERR_WORKSPACE
+    assert f(T=9000, ws=P) == moe.ERR_WORKSPACE and f(T=9000, n=8) == moe.ERR_WORKSPACE
+    assert f(T=9000, ws=odd) == moe.ERR_WORKSPACE and f(off=p, B=2, ws=P) == moe.ERR_WORKSPACE
     assert f(T=1 << 30, k=4) == UNS                   # T * k past 32 bits
     assert L.moe_balance_loss_workspace(-1, 8, 1) == 0
-    assert L.moe_balance_loss_workspace(0, 8, 1) > 0
+    assert L.moe_balance_loss_workspace(4, 8, 1) == 0 < L.moe_balance_loss_workspace(4, 8, 2)
 
     def g(lg=p, c=p, n=p, d=p, T=4, B=1):
         return L.moe_balance_loss_backward(lg, P, P, T, 8, 2, B, 1.0, c, n, P, d, P)
@@ -265,4 +266,4 @@ def test_binding_refusals(moe):
     with pytest.raises(ValueError):
         moe.balance_loss_backward(lg, s, 2, 1.0, mask, off)          # another number of sequences
     with pytest.raises(moe.MoeError):
-        moe.balance_loss(lg, idx, 1.0, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
+        moe.balance_loss(lg, idx, 1.0, mask, off, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
