@@ -59,7 +59,13 @@ __host__ __device__ constexpr int a_rows(int i) { return 32 << i; }
 constexpr int kGatherThreads = 64;      // warps 2 and 3
 constexpr int kGatherLag = 2;           // stages a gatherer runs ahead of its arrivals
 
-enum { MODE_STORE = 0, MODE_SWIGLU = 1, MODE_GEGLU = 2 };   // (the gate's activation)
+// a product stored in one of the three types, or gate|up with one of the gate
+// activations: fixed at compile time, which keeps the epilogues short
+enum { MODE_F32 = MOE_F32, MODE_BF16 = MOE_BF16, MODE_F16 = MOE_F16, MODE_SWIGLU, MODE_GEGLU };
+__host__ __device__ constexpr bool is_glu(int mode) { return mode == MODE_SWIGLU || mode == MODE_GEGLU; }
+__host__ __device__ constexpr int act_of(int mode) {
+  return mode == MODE_GEGLU ? MOE_ACT_GEGLU_TANH : MOE_ACT_SWIGLU;
+}
 
 template <int BN, bool SPLIT> struct Cfg {
   static constexpr int B_BYTES = BN * kBlock;
@@ -98,7 +104,6 @@ struct Params {
   int rows_per_group, scale_rows;
   void* out;
   float* out_s;              // GLU: [.][N / 128]
-  int out_dt;
   int wide;                  // every output row starts on a 32-byte boundary
   int* status;
   long long wait_limit;
@@ -151,19 +156,19 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 32 columns of this warp's 32 lanes. The registers are written until the
+// 16 columns of this warp's 32 lanes. The registers are written until the
 // wait, which takes them as operands, so that nothing reads them before it.
-__device__ __forceinline__ void tmem_ld32_start(uint32_t ta, uint32_t (&a)[32]) {
+__device__ __forceinline__ void tmem_ld_start(uint32_t ta, uint32_t (&a)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
       : "r"(ta)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&a)[32]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
                :
                : "memory");
 }
@@ -222,15 +227,38 @@ __device__ __forceinline__ Unit decode(const Params& p, const int* s_toff, const
 }
 
 // One value, rounded to the output type.
-__device__ __forceinline__ void store_one(const Params& p, size_t at, float v, bool& over) {
-  if (p.out_dt == MOE_F16) {
+template <int DT>
+__device__ __forceinline__ void store_one(void* out, size_t at, float v, bool& over) {
+  if constexpr (DT == MODE_F16) {
     const __half h = __float2half_rn(v);
     over |= (__half_as_ushort(h) & 0x7FFFu) >= 0x7C00u;
-    reinterpret_cast<__half*>(p.out)[at] = h;
-  } else if (p.out_dt == MOE_BF16) {
-    reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+    reinterpret_cast<__half*>(out)[at] = h;
+  } else if constexpr (DT == MODE_BF16) {
+    reinterpret_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
   } else {
-    reinterpret_cast<float*>(p.out)[at] = v;
+    reinterpret_cast<float*>(out)[at] = v;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack_two(float a, float b, uint32_t& hmax) {
+  if constexpr (DT == MODE_BF16) return pack_bf16x2(a, b);
+  const uint32_t v = pack_f16x2(a, b);
+  hmax = max(hmax, max(v & 0x7FFFu, (v >> 16) & 0x7FFFu));
+  return v;
+}
+
+// four consecutive values to one 8- or 16-byte aligned place (N % 4 == 0)
+template <int DT>
+__device__ __forceinline__ void store_four(void* out, size_t at, const float* v, bool& over) {
+  if constexpr (DT == MODE_F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at) =
+        make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t hmax = 0;
+    const uint2 o = make_uint2(pack_two<DT>(v[0], v[1], hmax), pack_two<DT>(v[2], v[3], hmax));
+    over |= hmax >= 0x7C00u;
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + at) = o;
   }
 }
 
@@ -238,7 +266,7 @@ __device__ __forceinline__ void store_one(const Params& p, size_t at, float v, b
 // row starts on a 32-byte boundary each lane stores whole sectors of its row;
 // elsewhere 16 columns at a time go through shared memory (the warp's patch),
 // and half a warp stores those of one row.
-template <int COLS, int LD>
+template <int DT, int COLS, int LD>
 __device__ __forceinline__ void store_rows(const Params& p, int r0, int m0, int nv, int c,
                                            const float (&acc)[COLS], float* patch, bool& over) {
   const int lane = threadIdx.x & 31;
@@ -254,13 +282,13 @@ __device__ __forceinline__ void store_rows(const Params& p, int r0, int m0, int 
       const int col = c + j + (lane & 15);
       for (int r = lane >> 4; r < 32 && m0 + r < nv; r += 2)
         if (col < p.N)
-          store_one(p, ((size_t)r0 + m0 + r) * p.N + col, patch[r * LD + (lane & 15)], over);
+          store_one<DT>(p.out, ((size_t)r0 + m0 + r) * p.N + col, patch[r * LD + (lane & 15)], over);
     }
     return;
   }
   if (m >= nv) return;
   const size_t at = ((size_t)r0 + m) * p.N + c;
-  if (p.out_dt == MOE_F32) {
+  if constexpr (DT == MODE_F32) {
     float* o = reinterpret_cast<float*>(p.out) + at;
 #pragma unroll
     for (int j = 0; j < COLS; j += 8) {
@@ -269,83 +297,149 @@ __device__ __forceinline__ void store_rows(const Params& p, int r0, int m0, int 
       for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(acc[j + i]);
       if (c + j < p.N) st32(o + j, v);
     }
-    return;
-  }
-  const bool f16 = p.out_dt == MOE_F16;
-  uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
-  uint32_t hmax = 0;
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
+    uint32_t hmax = 0;
 #pragma unroll
-  for (int j = 0; j < COLS; j += 16) {
-    if (c + j < p.N) {                             // N % 16 == 0
-      uint32_t v[8];
+    for (int j = 0; j < COLS; j += 16) {
+      if (c + j < p.N) {                           // N % 16 == 0
+        uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = acc[j + 2 * i], b = acc[j + 2 * i + 1];
-        v[i] = f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-        hmax = max(hmax, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+        for (int i = 0; i < 8; ++i) v[i] = pack_two<DT>(acc[j + 2 * i], acc[j + 2 * i + 1], hmax);
+        st32(o + j, v);
       }
-      st32(o + j, v);
     }
+    over |= hmax >= 0x7C00u;
   }
-  over |= f16 && hmax >= 0x7C00u;
+}
+
+// address of a shared-memory place in CTA `rank` of the cluster, and four floats there
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 f;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+               : "r"(addr)
+               : "memory");
+  return f;
 }
 
 // Split form: the sums of rows [0, nv) of the unit over the cluster's CTAs, a
-// warp per row, and their storage. Every CTA takes a share of the rows.
-template <int MODE, int BN, int LD>
-__device__ __forceinline__ void join_rows(const Params& p, const Unit& t, float* sums, int rank,
+// warp for RJ rows at a time (KU of the CTAs' sums of each on their way), and
+// their storage. Every CTA takes a share of the rows. The code is kept short:
+// it runs once per launch, and a body of several hundred instructions took
+// longer to arrive (a thousand cycles for four rows) than to execute. Bound by
+// the reads of the other CTAs' sums, about 25 bytes a cycle.
+template <int MODE, int BN, int LD, int RJ, int KU>
+__device__ __forceinline__ void join_rows(const Params& p, const Unit& t, uint32_t sums, int rank,
                                           bool& over) {
-  namespace cg = cooperative_groups;
-  constexpr int ACT = MODE == MODE_GEGLU ? MOE_ACT_GEGLU_TANH : MOE_ACT_SWIGLU;
-  cg::cluster_group cluster = cg::this_cluster();
-  constexpr int V = BN / 32;               // columns per lane
+  constexpr int V = BN / 32;               // columns per lane, in runs of 128 columns
   const int warp = (threadIdx.x >> 5) - kAccWarp0, lane = threadIdx.x & 31;
-  for (int r = rank * kAccWarps + warp; r < t.nv; r += p.split * kAccWarps) {
-    float v[V];
+  const bool four = p.N % 4 == 0;
+  const int step = p.split * kAccWarps;
+#pragma unroll 1
+  for (int r0 = rank * kAccWarps + warp; r0 < t.nv; r0 += step * RJ) {
+    float v[RJ][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.f;
-    for (int k = 0; k < p.split; ++k) {
-      const float* s = cluster.map_shared_rank(sums, k) + r * LD;
+    for (int j = 0; j < RJ; ++j)
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        // runs of 128 columns: gate|up holds 4 gate and their 4 up columns
-        const float4 f = *reinterpret_cast<const float4*>(s + i * 32 + lane * 4);
-        v[i] += f.x;
-        v[i + 1] += f.y;
-        v[i + 2] += f.z;
-        v[i + 3] += f.w;
-      }
+      for (int i = 0; i < V; ++i) v[j][i] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < p.split; k0 += KU) {
+      float4 f[RJ][KU][V / 4];
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+#pragma unroll
+        for (int k = 0; k < KU; ++k) {
+          // (rows past the tile and CTAs past the cluster: the first again)
+          const uint32_t s = map_rank(
+              sums + (uint32_t)((r0 + j * step < t.nv ? r0 + j * step : r0) * LD + lane * 4) * 4,
+              k0 + k < p.split ? k0 + k : rank);
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i) f[j][k][i] = ld_cluster(s + i * 512);
+        }
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+#pragma unroll
+        for (int k = 0; k < KU; ++k)
+          if (k0 + k < p.split) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+              v[j][4 * i] += f[j][k][i].x;
+              v[j][4 * i + 1] += f[j][k][i].y;
+              v[j][4 * i + 2] += f[j][k][i].z;
+              v[j][4 * i + 3] += f[j][k][i].w;
+            }
+          }
     }
-    const size_t row = (size_t)t.r0 + r;
-    if constexpr (MODE != MODE_STORE) {
-      float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = glu(ACT, v[i], v[4 + i]);
-        mx = fmaxf(mx, finite_abs(v[i]));
-      }
+    for (int j = 0; j < RJ; ++j) {
+      if (r0 + j * step >= t.nv) break;
+      const size_t row = (size_t)t.r0 + r0 + j * step;
+      if constexpr (is_glu(MODE)) {
+        // 4 gate columns and their 4 up columns per lane
+        float mx = 0.f, h[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float f = rscale_of(mx);
-      const size_t at = row * p.N + t.unit * kBlock + lane * 4;
-      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.out) + at) =
-          e4m3x4(code_arg(v[0], f), code_arg(v[1], f), code_arg(v[2], f), code_arg(v[3], f));
-      if (lane == 0) p.out_s[row * (p.N / kBlock) + t.unit] = scale_of(mx);
-    } else {
+        for (int i = 0; i < 4; ++i) {
+          h[i] = glu(act_of(MODE), v[j][i], v[j][4 + i]);
+          mx = fmaxf(mx, finite_abs(h[i]));
+        }
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int col = t.unit * BN + (i / 4) * 128 + lane * 4 + i % 4;
-        if (col < p.N) store_one(p, row * p.N + col, v[i], over);
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float f = rscale_of(mx);
+        const size_t at = row * p.N + t.unit * kBlock + lane * 4;
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.out) + at) =
+            e4m3x4(code_arg(h[0], f), code_arg(h[1], f), code_arg(h[2], f), code_arg(h[3], f));
+        if (lane == 0) p.out_s[row * (p.N / kBlock) + t.unit] = scale_of(mx);
+      } else {
+        const int col = t.unit * BN + lane * 4;
+        const size_t at = row * p.N + col;
+        if (four) {
+          if (col < p.N) store_four<MODE>(p.out, at, v[j], over);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (col + c < p.N) store_one<MODE>(p.out, at + c, v[j][c], over);
+        }
       }
     }
   }
+}
+
+// What a scaling thread needs of a unit: its row's scales, its columns' scales
+// (gate|up: those of the gate and of the up half), and the first of each.
+struct Lead {
+  const float *sa, *w0, *w1;
+  float a, b0, b1;
+  int r0, nv, unit;
+};
+template <bool GLU, int BN>
+__device__ __forceinline__ Lead lead(const Params& p, const Unit t, int m, int c0, int kb) {
+  Lead l;
+  l.r0 = t.r0;
+  l.nv = t.nv;
+  l.unit = t.unit;
+  int xrow = t.r0 + min(m, t.nv - 1);
+  if (GLU) xrow = (int)__ldg(p.row_map + xrow);
+  l.sa = p.xs + (size_t)xrow * p.KB + kb;
+  // (columns past N have no scale of their own and are not stored)
+  const int n = GLU ? t.unit : min((t.unit * BN + c0) / kBlock, p.scale_rows - 1);
+  l.w0 = p.ws + ((size_t)t.e * p.scale_rows + n) * p.KB + kb;
+  l.w1 = GLU ? l.w0 + (size_t)(p.N / kBlock) * p.KB : l.w0;
+  l.a = __ldg(l.sa);
+  l.b0 = __ldg(l.w0);
+  l.b1 = GLU ? __ldg(l.w1) : 0.f;
+  return l;
 }
 
 template <int MODE, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_tc_kernel(const __grid_constant__ Params p) {
-  constexpr bool GLU = MODE != MODE_STORE;
-  constexpr int ACT = MODE == MODE_GEGLU ? MOE_ACT_GEGLU_TANH : MOE_ACT_SWIGLU;
+  constexpr bool GLU = is_glu(MODE);
   using C = Cfg<BN, SPLIT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -536,31 +630,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     // the thread's columns: two runs of COLS / 2, one of gate and one of up
     // columns, or one after the other
-    const int c0 = MODE != MODE_STORE ? half * (COLS / 2) : half * COLS;
-    const int c1 = MODE != MODE_STORE ? BN / 2 + c0 : c0 + COLS / 2;
+    const int c0 = GLU ? half * (COLS / 2) : half * COLS;
+    const int c1 = GLU ? BN / 2 + c0 : c0 + COLS / 2;
     uint32_t it = 0, tiles = 0;
     bool ok = true, over = false;
-    // where a unit's scales are, and their first values: taken for the next
+    // a unit's rows and scales, their first values loaded: taken for the next
     // unit before the present one is stored
-    Unit t;
-    const float *sa, *w0, *w1;
-    float a = 0.f, b0 = 0.f, b1 = 0.f;
-    auto begin = [&](int u) {
-      t = decode(p, s_toff, s_roff, u);
-      int xrow = t.r0 + min(q * 32 + lane, t.nv - 1);
-      if (GLU) xrow = (int)__ldg(p.row_map + xrow);
-      sa = p.xs + (size_t)xrow * p.KB;
-      const float* wsc = p.ws + (size_t)t.e * p.scale_rows * p.KB;
-      // the scale rows of the two halves of the columns (columns past N have
-      // none of their own and are not stored)
-      const int n0 = GLU ? t.unit : min((t.unit * BN + c0) / kBlock, p.scale_rows - 1);
-      w0 = wsc + (size_t)n0 * p.KB;
-      w1 = GLU ? w0 + (size_t)(p.N / kBlock) * p.KB : w0;
-      a = __ldg(sa + kb_lo);
-      b0 = __ldg(w0 + kb_lo);
-      b1 = __ldg(w1 + kb_lo);
-    };
-    if (u0 < total) begin(u0);
+    Lead t{};
+    if (u0 < total) t = lead<GLU, BN>(p, decode(p, s_toff, s_roff, u0), q * 32 + lane, c0, kb_lo);
     for (int u = u0; u < total && ok; u += u_step, ++tiles) {
       const bool live = q * 32 < t.nv;            // some of the warp's lanes are rows
       const int m = q * 32 + lane;
@@ -568,30 +645,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
-        const float f0 = a * b0, f1 = a * b1;
+        const float f0 = t.a * t.b0, f1 = GLU ? t.a * t.b1 : f0;
         if (kb + 1 < kb_hi) {                     // the next block's, ahead of the wait
-          a = __ldg(sa + kb + 1);
-          b0 = __ldg(w0 + kb + 1);
-          b1 = __ldg(w1 + kb + 1);
+          t.a = __ldg(++t.sa);
+          t.b0 = __ldg(++t.w0);
+          if (GLU) t.b1 = __ldg(++t.w1);
         }
         const uint32_t b = it % C::NBUF;
         ok = mbar_wait_warp(smem_u32(acc_full + b), (it / C::NBUF) & 1, abort_flag, p.status, true,
                             p.wait_limit);
         if (!ok) break;
         tc_fence_after();
-        // a chunk of 32 columns is scaled while the next is on its way; the
+        // a chunk of 16 columns is scaled while the next is on its way; the
         // buffer is handed back as soon as the last has arrived
-        constexpr int NCH = COLS / 32, H = COLS / 2;
-        uint32_t d[2][32];
+        constexpr int NCH = COLS / 16, H = COLS / 2;
+        uint32_t d[2][16];
         if (live) {
-          tmem_ld32_start(tl + b * BN + c0, d[0]);
-          tmem_ld32_wait(d[0]);
+          tmem_ld_start(tl + b * BN + c0, d[0]);
+          tmem_ld_wait(d[0]);
         }
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
           if (live && j + 1 < NCH) {
-            const int c = (j + 1) * 32;
-            tmem_ld32_start(tl + b * BN + (c < H ? c0 + c : c1 + c - H), d[(j + 1) & 1]);
+            const int c = (j + 1) * 16;
+            tmem_ld_start(tl + b * BN + (c < H ? c0 + c : c1 + c - H), d[(j + 1) & 1]);
           }
           if (j + 1 == NCH) {
             tc_fence_before();
@@ -599,17 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
           }
           if (live) {
-            const float f = j * 32 < H ? f0 : f1;
+            const float f = j * 16 < H ? f0 : f1;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              fma2(acc[j * 32 + i], acc[j * 32 + i + 1], d[j & 1][i], d[j & 1][i + 1], f);
-            if (j + 1 < NCH) tmem_ld32_wait(d[(j + 1) & 1]);
+            for (int i = 0; i < 16; i += 2)
+              fma2(acc[j * 16 + i], acc[j * 16 + i + 1], d[j & 1][i], d[j & 1][i + 1], f);
+            if (j + 1 < NCH) tmem_ld_wait(d[(j + 1) & 1]);
           }
         }
       }
       if (!ok) break;
-      const Unit done = t;
-      if (!SPLIT && u + u_step < total) begin(u + u_step);
+      const int r0 = t.r0, nv = t.nv, unit = t.unit;
+      if (!SPLIT && u + u_step < total)
+        t = lead<GLU, BN>(p, decode(p, s_toff, s_roff, u + u_step), m, c0, kb_lo);
       if constexpr (SPLIT) {
         // every MMA of this CTA is done and every load consumed: the ring is free
         constexpr int H = COLS / 2;
@@ -620,9 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float4*>(o + (j < H ? c0 + j : c1 + j - H)) =
                 make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         }
-      } else if constexpr (MODE == MODE_STORE) {
+      } else if constexpr (!GLU) {
         if (live)
-          store_rows<COLS, C::PATCH_LD>(p, done.r0, q * 32, done.nv, done.unit * BN + c0, acc,
+          store_rows<MODE, COLS, C::PATCH_LD>(p, r0, q * 32, nv, unit * BN + c0, acc,
                                         s_patch + (warp - kAccWarp0) * 32 * C::PATCH_LD, over);
       } else {
         constexpr int H = COLS / 2;
@@ -630,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
 #pragma unroll
           for (int j = 0; j < H; ++j) {
-            acc[j] = glu(ACT, acc[j], acc[H + j]);
+            acc[j] = glu(act_of(MODE), acc[j], acc[H + j]);
             mx = fmaxf(mx, finite_abs(acc[j]));
           }
         }
@@ -643,11 +721,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(xchg));
         ok = mbar_wait_warp(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
         if (!ok) break;
-        if (m < done.nv) {
+        if (m < nv) {
           mx = fmaxf(am[m], am[BM + m]);
           const float r = rscale_of(mx);
-          uint8_t* o = reinterpret_cast<uint8_t*>(p.out) + ((size_t)done.r0 + m) * p.N +
-                       done.unit * kBlock + c0;
+          uint8_t* o = reinterpret_cast<uint8_t*>(p.out) + ((size_t)r0 + m) * p.N +
+                       unit * kBlock + c0;
 #pragma unroll
           for (int j = 0; j < H; j += 32) {
             uint32_t v[8];
@@ -663,19 +741,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (half == 0)
-            p.out_s[((size_t)done.r0 + m) * (p.N / kBlock) + done.unit] = scale_of(mx);
+            p.out_s[((size_t)r0 + m) * (p.N / kBlock) + unit] = scale_of(mx);
         }
       }
     }
     if constexpr (SPLIT) {
       cooperative_groups::this_cluster().sync();     // every CTA's sums are in place
       // (a CTA that gave up waiting has left none; the status says so)
-      if (u0 < total)
-        join_rows<MODE, BN, C::SUM_LD>(p, decode(p, s_toff, s_roff, u0),
-                                       reinterpret_cast<float*>(smem), rank, over);
+      if (u0 < total) {
+        if (p.split <= 2)
+          join_rows<MODE, BN, C::SUM_LD, GLU ? 1 : 4, 2>(p, decode(p, s_toff, s_roff, u0), st_base,
+                                                         rank, over);
+        else
+          join_rows<MODE, BN, C::SUM_LD, 1, GLU ? 4 : 8>(p, decode(p, s_toff, s_roff, u0), st_base,
+                                                         rank, over);
+      }
       cooperative_groups::this_cluster().sync();     // no CTA leaves while its sums are read
     }
-    if (MODE == MODE_STORE && over) report_status(p.status, MOE_ERR_RANGE);
+    if (MODE == MODE_F16 && over) report_status(p.status, MOE_ERR_RANGE);
   }
   tc_fence_before();
   __syncthreads();
@@ -737,10 +820,10 @@ static bool row_map2d(CUtensorMap* m, const void* base, long long rows, int K, i
 template <int MODE>
 static cudaError_t run(Params& p, const void* x, long long x_rows, const void* w, long long tiles,
                        cudaStream_t s) {
-  constexpr bool GLU = MODE != MODE_STORE;
+  constexpr bool GLU = is_glu(MODE);
   constexpr int BNS = GLU ? 256 : 128;                       // columns of the split form
   p.wait_limit = wait_cycles();
-  const int esize = GLU ? 1 : p.out_dt == MOE_F32 ? 4 : 2;
+  const int esize = GLU ? 1 : MODE == MODE_F32 ? 4 : 2;
   p.wide = (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) && ((long long)p.N * esize) % 32 == 0;
   // rows are addressed by 32-bit coordinates
   if ((long long)p.E * p.rows_per_group > 0x7fffffffLL) return cudaErrorNotSupported;
@@ -791,9 +874,11 @@ cudaError_t launch_fp8_matmul_tc(const void* a, const float* sa, const void* b, 
   p.rows_per_group = N;
   p.scale_rows = (N + kBlock - 1) / kBlock;
   p.out = y;
-  p.out_dt = out_dt;
   p.status = status;
-  return run<MODE_STORE>(p, a, M, b, ((long long)M + BM - 1) / BM, s);
+  const long long tiles = ((long long)M + BM - 1) / BM;
+  if (out_dt == MOE_BF16) return run<MODE_BF16>(p, a, M, b, tiles, s);
+  if (out_dt == MOE_F16) return run<MODE_F16>(p, a, M, b, tiles, s);
+  return run<MODE_F32>(p, a, M, b, tiles, s);
 }
 
 cudaError_t launch_swiglu_fp8_tc(const void* xq, const float* xs, int T, const uint32_t* row_map,
@@ -839,9 +924,8 @@ cudaError_t launch_down_fp8_tc(const void* hq, const float* hs, const int32_t* r
   p.rows_per_group = ex.d;
   p.scale_rows = ex.d / kBlock;
   p.out = ys;
-  p.out_dt = MOE_F16;
   p.status = status;
-  return run<MODE_STORE>(p, hq, R, ex.w_dn, max_tiles(R, ex.E, BM), s);
+  return run<MODE_F16>(p, hq, R, ex.w_dn, max_tiles(R, ex.E, BM), s);
 }
 
 }  // namespace moe
