@@ -57,7 +57,6 @@ constexpr int A_BYTES = BM * kBlock;
 constexpr int A_MAPS = 3;
 __host__ __device__ constexpr int a_rows(int i) { return 32 << i; }
 constexpr int kGatherThreads = 64;      // warps 2 and 3
-constexpr int kGatherLag = 2;           // stages a gatherer runs ahead of its arrivals
 
 // a product stored in one of the three types, or gate|up with one of the gate
 // activations: fixed at compile time, which keeps the epilogues short
@@ -83,7 +82,6 @@ template <int BN, bool SPLIT> struct Cfg {
   static constexpr int SUM_LD = BN + 4;             // rows 4 banks apart: 16-byte stores
   static_assert(!SPLIT || BM * SUM_LD * 4 <= NS * STAGE, "the sums fit the ring");
   static_assert(SMEM <= 232448, "shared memory per CTA");
-  static_assert(kGatherLag < NS, "a gathered stage is handed over before its ring slot is due");
 };
 
 struct Params {
@@ -152,8 +150,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// arrives on the barrier (one of its count) once this thread's copies have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 columns of this warp's 32 lanes. The registers are written until the
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(smem_u32(full + i), GLU ? 3 : 1);    // the TMA warp, the two gatherers
+      mbar_init(smem_u32(full + i), 1 + (GLU ? kGatherThreads : 0));
       mbar_init(smem_u32(empty + i), 1);
     }
     for (int i = 0; i < C::NBUF; ++i) {
@@ -554,11 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst0 = st_base + row0 * kBlock + ((ch ^ row0) << 4);
       uint32_t it = 0;
       bool ok = true;
-      auto arrive = [&](uint32_t i) {          // this warp's copies of k-block i have landed
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(full + i % C::NS));
-      };
       for (int u = u0; u < total && ok; u += u_step) {
         const Unit t = decode(p, s_toff, s_roff, u);
         uint32_t rows[NR];
@@ -578,15 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < NR; ++i)
             if (row0 + i * RSTEP < t.nv)
               cp_async16(dst + i * (RSTEP * kBlock), src + (size_t)rows[i] * p.K);
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (it >= (uint32_t)kGatherLag) {
-            cp_async_wait<kGatherLag>();
-            arrive(it - kGatherLag);
-          }
+          cp_async_arrive(smem_u32(full + s));
         }
       }
-      cp_async_wait<0>();
-      for (uint32_t i = it < (uint32_t)kGatherLag ? 0 : it - kGatherLag; i < it; ++i) arrive(i);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -608,6 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_warp(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
                               p.wait_limit);
           if (!ok) break;
+          // (the gathered rows were written by ordinary copies)
+          if (GLU) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           tc_fence_after();
           const uint32_t off = s * kStage16;
           mma_block(tm + b * BN, alo0 + off, ahi, blo0 + off, bhi, idesc);

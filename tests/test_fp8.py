@@ -191,7 +191,8 @@ def _check_matmul(y, a, sa, b, sb, dtype):
 MATMUL_SIZES = [(1, 1, 16), (33, 20, 16), (1, 128, 128), (2, 17, 48), (7, 200, 272), (8, 512, 7168),
                 (9, 256, 384), (33, 1000, 2064), (64, 96, 128), (100, 333, 656), (128, 256, 256),
                 (129, 640, 1024), (300, 257, 512), (511, 1024, 1152),
-                (40, 640, 4112), (1030, 2100, 400), (700, 4096, 256)]
+                (40, 640, 4112), (1030, 2100, 400), (700, 4096, 256), (2000, 1300, 128),
+                (900, 5000, 320)]
 
 
 @gpu
@@ -309,7 +310,7 @@ STAGES_TC = [  # T, E, k, d, F, skew
     (1, 8, 2, 128, 128, 0.0), (5, 4, 3, 256, 384, 0.0), (33, 16, 4, 384, 128, 0.0),
     (300, 6, 2, 256, 128, 0.0), (200, 32, 4, 128, 256, 0.2), (129, 1, 1, 640, 256, 0.0),
     (400, 3, 2, 1152, 640, 0.3), (37, 64, 8, 256, 128, 0.05), (70, 2, 1, 2176, 128, 0.0),
-    (1000, 16, 4, 256, 640, 0.1)]
+    (1000, 16, 4, 256, 640, 0.1), (600, 40, 4, 128, 512, 0.02), (500, 24, 6, 2048, 128, 0.0)]
 
 
 @gpu
