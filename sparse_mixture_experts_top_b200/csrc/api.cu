@@ -139,10 +139,16 @@ static moe_status check_fp8_stage(const moe_experts* ex, int BM, int T, int k, i
   return MOE_OK;
 }
 
-// The regime of a grouped fp8 call
-static int resolve_fp8(int regime, long long R, int E) {
+// The regime of a grouped fp8 call with N output columns. AUTO keeps the
+// weight-streaming kernel while its CTAs (16 columns of one expert each) are one
+// wave, three to an SM, of about one row to an expert; the tensor cores take
+// the rest. Measured on one B200, gate|up: one token through 8 of 128 experts
+// of 768 features (384 CTAs) 10.1 against 11.3 us, two tokens (768) 18.5 against
+// 16.2; 64 tokens over 16 experts of 512 (4 rows to an expert) 10.5 against 8.5.
+static int resolve_fp8(int regime, long long R, int E, int N) {
   if (regime != MOE_REGIME_AUTO) return regime;
-  return R <= 64 || R < E ? MOE_REGIME_GEMV : MOE_REGIME_TC;
+  const long long ctas = (R < E ? R : E) * ((N + 15) / 16);
+  return ctas <= 3 * 148 && R <= 2LL * E ? MOE_REGIME_GEMV : MOE_REGIME_TC;
 }
 
 static cudaError_t swiglu_fp8(int rg, const void* xq, const float* xs, const uint32_t* rmap,
@@ -387,12 +393,16 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
   if (!a || !sa || !b || !sb || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
     return MOE_ERR_INVALID_ARG;
-  // Up to 8 rows the weight-streaming kernel is the faster one (one row, N = 4096,
-  // K = 7168: 8 against 9 us on one B200); past them it reads the weights again
-  // for every 32 rows, and keeps ahead only where that is little (N = K = 512:
-  // 5 against 8 us at 256 rows; N = K = 2048: 6.5 against 5.6 us at 32)
-  const long long passes = ((long long)M + 31) / 32;
-  if (M > 8 && passes * N * K > (1 << 21))
+  // Up to 8 rows the weight-streaming kernel is the faster one until the weights
+  // are large (one row, on one B200: N = 256, K = 2048 2.9 against 4.6 us,
+  // 4096 x 7168 8 against 9, 8192 x 8192 18.7 against 15.7). Past 8 rows it reads
+  // them again for every 32 and keeps ahead only where they are small and K is
+  // short (256 rows, N = K = 512: 4.8 against 6.8 us; 9 rows, N = 128, K = 7168:
+  // 10.4 against 5.8).
+  const long long weights = (long long)N * K;
+  const bool stream = M <= 8 ? weights <= (1LL << 25)
+                             : K <= 1024 && ((long long)M + 31) / 32 * weights <= (1LL << 21);
+  if (!stream)
     return launched(launch_fp8_matmul_tc(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
                                          (cudaStream_t)stream));
   return launched(launch_fp8_matmul_stream(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
@@ -409,7 +419,7 @@ moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_
   if (!xq || !xs || !row_map || !row_off || !tile_off || !hq || !hs) return MOE_ERR_INVALID_ARG;
   if (!aligned16(xq) || !aligned16(xs) || !aligned16(hq) || !aligned16(hs))
     return MOE_ERR_INVALID_ARG;
-  int rg = resolve_fp8(regime, (long long)T * k, experts->E);
+  int rg = resolve_fp8(regime, (long long)T * k, experts->E, experts->F);
   if (regime == MOE_REGIME_AUTO && BM != tc_block_m()) rg = MOE_REGIME_GEMV;
   if (rg == MOE_REGIME_TC && BM != tc_block_m()) return MOE_ERR_INVALID_ARG;
   return launched(swiglu_fp8(rg, xq, xs, row_map, row_off, tile_off, BM, T, T * k, *experts, hq,
@@ -425,7 +435,7 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
   if (T == 0) return MOE_OK;
   if (!hq || !hs || !row_off || !tile_off || !ys) return MOE_ERR_INVALID_ARG;
   if (!aligned16(hq) || !aligned16(hs) || !aligned16(ys)) return MOE_ERR_INVALID_ARG;
-  int rg = resolve_fp8(regime, (long long)T * k, experts->E);
+  int rg = resolve_fp8(regime, (long long)T * k, experts->E, experts->d);
   if (regime == MOE_REGIME_AUTO && BM != tc_block_m()) rg = MOE_REGIME_GEMV;
   if (rg == MOE_REGIME_TC && BM != tc_block_m()) return MOE_ERR_INVALID_ARG;
   return launched(down_fp8(rg, hq, hs, row_off, tile_off, BM, T * k, *experts, ys, status_ptr(),
@@ -573,8 +583,16 @@ moe_status moe_forward_layout(int T, int d, int E, int k, int F, moe_dtype dt, m
   // fp16 (16-bit activations) or fp32; e4m3 experts: codes and their scales
   L.h = take(wfmt == MOE_W_F8 ? fp8_bytes(R, F) : (size_t)R * F * a);
   L.ys = take((size_t)R * d * a);     // fp16 (16-bit activations) or fp32
-  L.regime = wfmt == MOE_W_F8 ? resolve_fp8(regime, R, E) : resolve_regime(regime, R, E, dt, d, F, wfmt, decode_fused_ok(T, k, E, d, F, wfmt, dt));
-  L.BM = block_m_for(L.regime, R, E);
+  if (wfmt == MOE_W_F8) {
+    // (gate|up's; under AUTO the down product has a choice of its own, and both
+    // kernels take the tensor cores' tiles)
+    L.regime = resolve_fp8(regime, R, E, F);
+    L.BM = tc_block_m();
+  } else {
+    L.regime = resolve_regime(regime, R, E, dt, d, F, wfmt,
+                              decode_fused_ok(T, k, E, d, F, wfmt, dt));
+    L.BM = block_m_for(L.regime, R, E);
+  }
   // fp16 token rows: x converted (weight-streaming), or permuted (the
   // one-launch path), or gathered in sorted row order (tensor cores)
   // (e4m3 experts: the token rows' codes and scales, in token order)
@@ -656,7 +674,7 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
                         stp, s)) !=
         cudaSuccess)
       return launched(e);
-    if ((e = down_fp8(regime_run, h, hs, roff, toff, L.BM, (int)R, *experts, ys, stp, s)) != cudaSuccess)
+    if ((e = down_fp8(resolve_fp8(regime, R, E, d), h, hs, roff, toff, L.BM, (int)R, *experts, ys, stp, s)) != cudaSuccess)
       return launched(e);
   } else if (regime_run == MOE_REGIME_TC) {
     // h stays in the q4 dequant's permuted K order between the two kernels

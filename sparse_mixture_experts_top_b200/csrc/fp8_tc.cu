@@ -448,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + C::NS;                                          // [NS]
   uint64_t* acc_full = empty + C::NS;                                      // [NBUF]
   uint64_t* acc_empty = acc_full + C::NBUF;                                // [NBUF]
-  uint64_t* xchg = acc_empty + C::NBUF;                                    // [1]
+  uint64_t* rows_full = acc_empty + C::NBUF;                               // [NS]
+  uint64_t* xchg = rows_full + C::NS;                                      // [1]
   uint64_t* drain = xchg + 1;                                              // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -462,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(smem_u32(full + i), 1 + (GLU ? kGatherThreads : 0));
+      mbar_init(smem_u32(full + i), 1);                     // TMA
+      mbar_init(smem_u32(rows_full + i), kGatherThreads);   // gathered token rows
       mbar_init(smem_u32(empty + i), 1);
     }
     for (int i = 0; i < C::NBUF; ++i) {
@@ -537,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-      for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
-        const uint32_t last = it - 1 - i;
+        for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
+          const uint32_t last = it - 1 - i;
           mbar_wait(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status, false);
         }
       }
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < NR; ++i)
             if (row0 + i * RSTEP < t.nv)
               cp_async16(dst + i * (RSTEP * kBlock), src + (size_t)rows[i] * p.K);
-          cp_async_arrive(smem_u32(full + s));
+          cp_async_arrive(smem_u32(rows_full + s));
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -596,6 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ok = mbar_wait_warp(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
                               p.wait_limit);
+          if (ok && GLU)
+            ok = mbar_wait_warp(smem_u32(rows_full + s), (it / C::NS) & 1, abort_flag, p.status,
+                                true, p.wait_limit);
           if (!ok) break;
           // (the gathered rows were written by ordinary copies)
           if (GLU) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -192,7 +192,7 @@ MATMUL_SIZES = [(1, 1, 16), (33, 20, 16), (1, 128, 128), (2, 17, 48), (7, 200, 2
                 (9, 256, 384), (33, 1000, 2064), (64, 96, 128), (100, 333, 656), (128, 256, 256),
                 (129, 640, 1024), (300, 257, 512), (511, 1024, 1152),
                 (40, 640, 4112), (1030, 2100, 400), (700, 4096, 256), (2000, 1300, 128),
-                (900, 5000, 320)]
+                (900, 5000, 320), (3000, 1100, 1040)]
 
 
 @gpu
@@ -310,7 +310,9 @@ STAGES_TC = [  # T, E, k, d, F, skew
     (1, 8, 2, 128, 128, 0.0), (5, 4, 3, 256, 384, 0.0), (33, 16, 4, 384, 128, 0.0),
     (300, 6, 2, 256, 128, 0.0), (200, 32, 4, 128, 256, 0.2), (129, 1, 1, 640, 256, 0.0),
     (400, 3, 2, 1152, 640, 0.3), (37, 64, 8, 256, 128, 0.05), (70, 2, 1, 2176, 128, 0.0),
-    (1000, 16, 4, 256, 640, 0.1), (600, 40, 4, 128, 512, 0.02), (500, 24, 6, 2048, 128, 0.0)]
+    (1000, 16, 4, 256, 640, 0.1), (600, 40, 4, 128, 512, 0.02), (500, 24, 6, 2048, 128, 0.0),
+    # many rows to an expert: pairs of tiles, one expert of few rows
+    (2000, 3, 2, 640, 640, 0.0), (1500, 5, 2, 768, 512, 2.0), (3333, 1, 1, 512, 384, 0.0)]
 
 
 @gpu
@@ -363,8 +365,8 @@ def test_forward_with_f8_experts(moe, T, E, k, d, F, act):
     logits, idx, w = moe.route(L.x, L.w_router, L.router_bias, k)
     st = moe.sort_rows(idx, E, lay.BM)
     xq, xs = moe.quantize_fp8(L.x)
-    hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, k, L.experts, lay.regime)
-    ys = moe.grouped_down_fp8(hq, hs, st, T, k, L.experts, lay.regime)
+    hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, k, L.experts)
+    ys = moe.grouped_down_fp8(hq, hs, st, T, k, L.experts)
     y2 = moe.combine(ys, st.inv_order, w, T, k, L.x.dtype)
     assert torch.equal(y, y2)
     _check_stages(L.experts, st, xq, xs, hq, hs, ys)
