@@ -400,9 +400,9 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
   // short (256 rows, N = K = 512: 4.8 against 6.8 us; 9 rows, N = 128, K = 7168:
   // 10.4 against 5.8).
   const long long weights = (long long)N * K;
-  const bool stream = M <= 8 ? weights <= (1LL << 25)
-                             : K <= 1024 && ((long long)M + 31) / 32 * weights <= (1LL << 21);
-  if (!stream)
+  const bool by_stream = M <= 8 ? weights <= (1LL << 25)
+                                : K <= 1024 && ((long long)M + 31) / 32 * weights <= (1LL << 21);
+  if (!by_stream)
     return launched(launch_fp8_matmul_tc(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
                                          (cudaStream_t)stream));
   return launched(launch_fp8_matmul_stream(a, sa, b, sb, M, N, K, dt, y, status_ptr(),
