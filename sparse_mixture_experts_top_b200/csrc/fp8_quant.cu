@@ -13,87 +13,118 @@
 namespace moe {
 namespace fp8 {
 
-// 16 consecutive elements as floats
+// 16 consecutive elements as they are stored, the largest magnitude of the
+// finite ones, and their codes. A thread with an infinity or a NaN (the
+// largest bit pattern says so) goes through its elements one by one; the
+// others need no test per element, and 16-bit magnitudes are compared two to
+// an instruction, as integers.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
-  if constexpr (sizeof(T) == 4) {
+struct Elems {
+  static constexpr bool kWide = sizeof(T) == 4;
+  static constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+  uint32_t u[kWide ? 16 : 8];
+  bool odd;                          // some element is not finite
+
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 a = ldg_nc_v4(p + 4 * i);
-      v[4 * i] = __uint_as_float(a.x);
-      v[4 * i + 1] = __uint_as_float(a.y);
-      v[4 * i + 2] = __uint_as_float(a.z);
-      v[4 * i + 3] = __uint_as_float(a.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 a = ldg_nc_v4(p + 8 * i);
-      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 f;
-        if constexpr (std::is_same<T, __half>::value)
-          f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-        else
-          f = bf16x2_to_f32x2(u[j]);
-        v[8 * i + 2 * j] = f.x;
-        v[8 * i + 2 * j + 1] = f.y;
-      }
+    for (int i = 0; i < (kWide ? 4 : 2); ++i) {
+      const uint4 a = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + i);
+      u[4 * i] = a.x;
+      u[4 * i + 1] = a.y;
+      u[4 * i + 2] = a.z;
+      u[4 * i + 3] = a.w;
     }
   }
-}
-
-__device__ __forceinline__ float amax16(const float (&v)[16]) {
-  float m = 0.f;
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[i]));
-  return m;
-}
-
-__device__ __forceinline__ uint4 codes16(const float (&v)[16], float r) {
-  uint32_t c[4];
+    for (int i = 0; i < (kWide ? 16 : 8); ++i) u[i] = 0;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (kWide) return __uint_as_float(u[i]);
+    const uint32_t h = u[i / 2] >> (i % 2 * 16) & 0xFFFFu;
+    if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((uint16_t)h));
+    return bf16_bits_to_f32(h);
+  }
+  __device__ __forceinline__ float amax() {
+    float m = 0.f;
+    if constexpr (kWide) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = e4m3x4(code_arg(v[4 * i], r), code_arg(v[4 * i + 1], r), code_arg(v[4 * i + 2], r),
-                  code_arg(v[4 * i + 3], r));
-  return make_uint4(c[0], c[1], c[2], c[3]);
-}
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(at(i)));     // passes over NaN
+      odd = m > FLT_MAX;
+    } else {
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x = __vmaxu2(x, u[i] & 0x7FFF7FFFu);
+      const uint32_t h = max(x & 0xFFFFu, x >> 16);
+      odd = h >= kInf;
+      m = std::is_same<T, __half>::value ? __half2float(__ushort_as_half((uint16_t)h))
+                                         : bf16_bits_to_f32(h);
+    }
+    if (odd) {
+      m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(at(i)));
+    }
+    return m;
+  }
+  __device__ __forceinline__ uint4 codes(float r) const {
+    uint32_t c[4];
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i] = e4m3x4(code_arg(at(4 * i), r), code_arg(at(4 * i + 1), r),
+                      code_arg(at(4 * i + 2), r), code_arg(at(4 * i + 3), r));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i] = e4m3x4(at(4 * i) * r, at(4 * i + 1) * r, at(4 * i + 2) * r, at(4 * i + 3) * r);
+    }
+    return make_uint4(c[0], c[1], c[2], c[3]);
+  }
+};
 
-// One scale per row and 128 columns: 8 threads x 16 elements per group.
+// One scale per row and 128 columns: 8 threads x 16 elements per group, UN
+// groups per thread whose loads go out together.
+template <typename T>
+constexpr int row_groups() { return sizeof(T) == 4 ? 1 : 2; }
+
 template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x, long long groups,
                                                          int K, int KB, uint8_t* __restrict__ q,
                                                          float* __restrict__ s) {
+  constexpr int UN = row_groups<T>();
   pdl_wait();
   pdl_launch();
-  const long long g = ((long long)blockIdx.x * 256 + threadIdx.x) >> 3;
   const int l8 = threadIdx.x & 7;
-  const bool in = g < groups;
-  long long row = 0;
-  int kb = 0;
-  if (groups <= 0x7fffffffLL) {          // a 32-bit division where it fits
-    row = (uint32_t)g / (uint32_t)KB;
-    kb = (int)((uint32_t)g - (uint32_t)row * (uint32_t)KB);
-  } else {
-    row = g / KB;
-    kb = (int)(g - row * KB);
-  }
-  const int col = kb * kBlock + l8 * 16;
-  const bool live = in && col < K;        // K % 16 == 0: all 16 or none
-  const size_t at = (size_t)row * K + col;
-  float v[16];
-  if (live) {
-    load16(x + at, v);
-  } else {
+  Elems<T> v[UN];
+  size_t at[UN];
+  bool live[UN];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  for (int j = 0; j < UN; ++j) {
+    const long long g = ((long long)blockIdx.x * UN + j) * 32 + (threadIdx.x >> 3);
+    long long row;
+    int kb;
+    if (groups <= 0x7fffffffLL) {          // a 32-bit division where it fits
+      row = (uint32_t)g / (uint32_t)KB;
+      kb = (int)((uint32_t)g - (uint32_t)row * (uint32_t)KB);
+    } else {
+      row = g / KB;
+      kb = (int)(g - row * KB);
+    }
+    const int col = kb * kBlock + l8 * 16;
+    live[j] = g < groups && col < K;        // K % 16 == 0: all 16 or none
+    at[j] = (size_t)row * K + col;
+    if (live[j]) v[j].load(x + at[j]); else v[j].zero();
   }
-  float m = amax16(v);
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (live) *reinterpret_cast<uint4*>(q + at) = codes16(v, rscale_of(m));
-  if (in && l8 == 0) s[g] = scale_of(m);
+  for (int j = 0; j < UN; ++j) {
+    float m = v[j].amax();
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (live[j]) *reinterpret_cast<uint4*>(q + at[j]) = v[j].codes(rscale_of(m));
+    const long long g = ((long long)blockIdx.x * UN + j) * 32 + (threadIdx.x >> 3);
+    if (g < groups && l8 == 0) s[g] = scale_of(m);
+  }
 }
 
 // One scale per 128 x 128 block: one CTA of 256 threads per block, 32 rows at
@@ -109,20 +140,15 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__
   const int rb = blockIdx.x / KB;
   const int col = kb * kBlock + (threadIdx.x & 7) * 16;
   const int r0 = rb * kBlock + (threadIdx.x >> 3);
-  float v[4][16];
+  Elems<T> v[4];
   float m = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = r0 + 32 * j;
-    if (r < rows && col < K) {
-      load16(x + (size_t)r * K + col, v[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
-    }
+    if (r < rows && col < K) v[j].load(x + (size_t)r * K + col); else v[j].zero();
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) m = fmaxf(m, amax16(v[j]));
+  for (int j = 0; j < 4; ++j) m = fmaxf(m, v[j].amax());
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
@@ -134,7 +160,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int rr = r0 + 32 * j;
-    if (rr < rows && col < K) *reinterpret_cast<uint4*>(q + (size_t)rr * K + col) = codes16(v[j], r);
+    if (rr < rows && col < K) *reinterpret_cast<uint4*>(q + (size_t)rr * K + col) = v[j].codes(r);
   }
   if (threadIdx.x == 0) s[(size_t)rb * KB + kb] = scale_of(m);
 }
@@ -145,7 +171,8 @@ static cudaError_t run(const void* x, int rows, int K, int block, void* q, float
   const int KB = (K + kBlock - 1) / kBlock;
   if (block == 1) {
     const long long groups = (long long)rows * KB;
-    const long long ctas = (groups * 8 + 255) / 256;
+    const long long per_cta = 32 * row_groups<T>();
+    const long long ctas = (groups + per_cta - 1) / per_cta;
     if (ctas > 0x7fffffffLL) return cudaErrorNotSupported;
     launch_pdl(quant_rows_kernel<T>, (unsigned)ctas, 256, 0, st, (const T*)x, groups, K, KB,
                (uint8_t*)q, s);

@@ -39,6 +39,20 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// whether the phase has completed, at once (try_wait may suspend the thread for
+// a while of the hardware's choosing)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // try_wait with a suspend-time hint: a thread whose phase is not complete
 // sleeps until it completes or about `ns` nanoseconds pass, instead of
 // spinning and taking issue slots from the warps that do the work
@@ -60,16 +74,17 @@ __device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity, ui
 // launch's bound (Params::wait_limit); the waits for copies and MMAs still in
 // flight before the CTA exits keep the full bound, so that nothing lands in
 // shared memory or TMEM after the CTA has released it. A bound below ~50 us
-// also drops the sleep hint, so the wait notices its deadline promptly.
+// polls instead of suspending the thread, so the wait notices its deadline
+// promptly.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int* status, bool honor_abort = true,
                                           long long limit = kWaitCycles) {
-  if (mbar_try(bar, parity)) return true;
-  const long long t0 = clock64();
   const bool sleep = limit >= 100000;
+  if (sleep ? mbar_try(bar, parity) : mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
   const uint32_t af = smem_u32(const_cast<const int*>(abort_flag));
   for (;;) {
-    if (sleep ? mbar_try_sleep(bar, parity, 20000u) : mbar_try(bar, parity)) return true;
+    if (sleep ? mbar_try_sleep(bar, parity, 20000u) : mbar_test(bar, parity)) return true;
     uint32_t aborting;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(aborting) : "r"(af) : "memory");
     if (honor_abort && aborting) return false;

@@ -133,7 +133,8 @@ def test_quantize_matches_the_definition(moe, dtype, rows, K, block):
 
 
 @gpu
-def test_quantize_special_values(moe):
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_quantize_special_values(moe, dtype):
     """Infinities and NaN become NaN codes and leave the scale alone; zero and
     tiny groups take the floor's scale; negative zero stays a zero."""
     x = torch.randn(6, 256)
@@ -141,14 +142,16 @@ def test_quantize_special_values(moe):
     x[2] = 0
     x[3, :128] = 1e-38
     x[4, :128] = float("nan")
-    x[5, 0], x[5, 1] = 3.4e38, -0.0
-    q, s = moe.quantize_fp8(x.to(DEV))
+    x[5, 0], x[5, 1] = torch.finfo(dtype).max, -0.0
+    gx = x.to(dtype).to(DEV)
+    x = x.to(dtype).float()
+    q, s = moe.quantize_fp8(gx)
     rq, rs = quantize_ref(x.numpy())
     np.testing.assert_array_equal(s.cpu().numpy(), rs)
     np.testing.assert_array_equal(values(q), rq)
     assert np.isnan(values(q)[0, 3]) and np.isfinite(rs).all()
     # one bad element in a block spoils only itself
-    q, s = moe.quantize_fp8(x.to(DEV), 128)
+    q, s = moe.quantize_fp8(gx, 128)
     rq, rs = quantize_ref(x.numpy(), 128)
     np.testing.assert_array_equal(s.cpu().numpy(), rs)
     np.testing.assert_array_equal(values(q), rq)
@@ -348,6 +351,56 @@ def test_pack_gate_up_f8(moe):
     sg, su = ex.s_gu[:, :1].contiguous(), ex.s_gu[:, 1:].contiguous()
     w, s, b = moe.pack_gate_up("f8", g, u, s_g=sg, s_u=su)
     assert torch.equal(w, ex.w_gu) and torch.equal(s, ex.s_gu) and b is None
+
+
+@gpu
+def test_waits_that_run_out(moe):
+    """With a bound of one cycle the first wait of a tensor-core kernel that is
+    not met gives up, the status says so, and the next call is as before."""
+    a, sa, b, sb = _operands(moe, 100, 640, 4096, 1)          # the split form
+    a2, sa2, b2, sb2 = _operands(moe, 1000, 3000 // 8 * 8, 512, 2)   # the persistent one
+    ex = _experts(16, 512, 256, 7)
+    idx = mi.random_topk_idx(300, 16, 4, 1).to(DEV)
+    st = moe.sort_rows(idx, 16, 128)
+    xq, xs = moe.quantize_fp8(torch.randn(300, 512, device=DEV))
+    hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, 4, ex, moe.REGIME_TC)
+    calls = [lambda: (moe.fp8_matmul(a, sa, b, sb),), lambda: (moe.fp8_matmul(a2, sa2, b2, sb2),),
+             lambda: moe.grouped_swiglu_fp8(xq, xs, st, 4, ex, moe.REGIME_TC),
+             lambda: (moe.grouped_down_fp8(hq, hs, st, 300, 4, ex, moe.REGIME_TC),)]
+    for f in calls:
+        ref = f()
+        assert moe.device_status() == moe.OK
+        moe.set_wait_cycles(1)
+        try:
+            f()
+            assert moe.device_status() == moe.ERR_TIMEOUT
+        finally:
+            moe.set_wait_cycles(0)
+        for got, want in zip(f(), ref):
+            assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+        assert moe.device_status() == moe.OK
+
+
+@gpu
+def test_same_bits_every_time(moe):
+    """25 runs on the same inputs, the large forms among them."""
+    a, sa, b, sb = _operands(moe, 700, 1500, 1168, 3)
+    y = moe.fp8_matmul(a, sa, b, sb)
+    z = moe.fp8_matmul(a[:90].contiguous(), sa[:90].contiguous(), b, sb)
+    for _ in range(25):
+        assert torch.equal(moe.fp8_matmul(a, sa, b, sb), y)
+        assert torch.equal(moe.fp8_matmul(a[:90].contiguous(), sa[:90].contiguous(), b, sb), z)
+    ex = _experts(24, 768, 640, 7)
+    idx = mi.random_topk_idx(500, 24, 4, 1, 0.05).to(DEV)
+    st = moe.sort_rows(idx, 24, 128)
+    xq, xs = moe.quantize_fp8(torch.randn(500, 768, device=DEV))
+    for rg in (moe.REGIME_TC, moe.REGIME_GEMV):
+        hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, 4, ex, rg)
+        ys = moe.grouped_down_fp8(hq, hs, st, 500, 4, ex, rg)
+        for _ in range(25):
+            h2, s2 = moe.grouped_swiglu_fp8(xq, xs, st, 4, ex, rg)
+            assert torch.equal(h2.view(torch.uint8), hq.view(torch.uint8)) and torch.equal(s2, hs)
+            assert torch.equal(moe.grouped_down_fp8(hq, hs, st, 500, 4, ex, rg), ys)
 
 
 # ------------------------------------------------------------------ whole layer
