@@ -286,6 +286,8 @@ def combine(ys, inv_order, topk_w, T, k, dtype=torch.bfloat16, stream=None):
 
 F8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
+_F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
+_empty, _device, _raw_stream = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _on(*ts):
@@ -297,11 +299,11 @@ def _on(*ts):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("inputs must be contiguous CUDA tensors")
             if t.get_device() != dev:
-                if dev >= 0 or t.get_device() != torch.cuda.current_device():
+                if dev >= 0 or t.get_device() != _device():
                     raise ValueError(f"a tensor is on {t.device}, the call is for the current "
-                                     f"device, cuda:{torch.cuda.current_device()}")
+                                     f"device, cuda:{_device()}")
                 dev = t.get_device()
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return _raw_stream(dev)
 
 
 def _is(t, dtype, shape, what):
@@ -310,8 +312,9 @@ def _is(t, dtype, shape, what):
 
 
 def _codes(t, dims, what):
-    if t.dtype != F8 and t.dtype != torch.uint8:
-        raise TypeError(f"{what} must be e4m3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+    dt = t.dtype
+    if dt != F8 and dt != _U8:
+        raise TypeError(f"{what} must be e4m3 codes (float8_e4m3fn or uint8), got {dt}")
     if t.dim() != dims:
         raise ValueError(f"{what} must have {dims} dimensions, got {list(t.shape)}")
 
@@ -327,23 +330,26 @@ def quantize_fp8(x, block=1, stream=None):
     weights x [E, rows, K] (rows a multiple of 128 for block=128) gives a stack
     of scales."""
     raw = _on(x)
-    if x.dim() < 2:
-        raise ValueError(f"x must be [rows, K] or a stack of such, got {list(x.shape)}")
-    *lead, rows, K = x.shape
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError(f"x must be [rows, K] or a stack of such, got {list(shape)}")
+    rows, K = shape[-2:]
     if block != 1 and block != FP8_BLOCK:
         raise ValueError(f"block must be 1 or {FP8_BLOCK}, got {block}")
-    n = rows
-    if lead:
+    n, groups = rows, (rows if block == 1 else -(-rows // FP8_BLOCK))
+    q = torch.empty_like(x, dtype=F8)
+    if len(shape) == 2:
+        s = _empty(groups, -(-K // FP8_BLOCK), dtype=_F32, device=x.device)
+    else:
         if block != 1 and rows % FP8_BLOCK:
             raise ValueError("a stack of weights needs rows in multiples of 128 (a block of "
                              "scales may not straddle two of them)")
         n = x.numel() // K if K else 0
-    q = torch.empty_like(x, dtype=F8)
-    s = x.new_empty((*lead, rows if block == 1 else -(-rows // FP8_BLOCK), -(-K // FP8_BLOCK)),
-                    dtype=torch.float32)
-    _check(lib.moe_quantize_fp8(x.data_ptr(), _dt(x), n, K, block, q.data_ptr(), s.data_ptr(),
-                                raw if stream is None else stream.cuda_stream),
-           "moe_quantize_fp8")
+        s = _empty(*shape[:-2], groups, -(-K // FP8_BLOCK), dtype=_F32, device=x.device)
+    st = lib.moe_quantize_fp8(x.data_ptr(), _dt(x), n, K, block, q.data_ptr(), s.data_ptr(),
+                              raw if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "moe_quantize_fp8")
     return q, s
 
 
@@ -354,19 +360,21 @@ def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
     _codes(a, 2, "a")
     _codes(b, 2, "b")
     M, K = a.shape
-    N, KB = b.shape
-    if KB != K:
-        raise ValueError(f"a is [{M}, {K}] and b [{N}, {KB}]: K differs")
+    N, Kb = b.shape
+    if Kb != K:
+        raise ValueError(f"a is [{M}, {K}] and b [{N}, {Kb}]: K differs")
     KB = -(-K // FP8_BLOCK)
-    _is(sa, torch.float32, (M, KB), "sa")
-    _is(sb, torch.float32, (-(-N // FP8_BLOCK), KB), "sb")
+    _is(sa, _F32, (M, KB), "sa")
+    _is(sb, _F32, (-(-N // FP8_BLOCK), KB), "sb")
+    dt = _dt_of(dtype)
     if out is None:
-        out = a.new_empty((M, N), dtype=dtype)
+        out = _empty(M, N, dtype=dtype, device=a.device)
     else:
         _is(out, dtype, (M, N), "out")
-    _check(lib.moe_fp8_matmul(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), M, N, K,
-                              _dt_of(dtype), out.data_ptr(),
-                              raw if stream is None else stream.cuda_stream), "moe_fp8_matmul")
+    st = lib.moe_fp8_matmul(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), M, N, K, dt,
+                            out.data_ptr(), raw if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "moe_fp8_matmul")
     return out
 
 
@@ -381,8 +389,8 @@ def _f8_experts(ex) -> Experts:
         raise ValueError("f8 experts: w_gu must be [E, 2F, d] and w_dn [E, d, F]")
     _codes(w_gu, 3, "w_gu")
     _codes(w_dn, 3, "w_dn")
-    _is(s_gu, torch.float32, (E, 2 * F // B, d // B), "s_gu")
-    _is(s_dn, torch.float32, (E, d // B, F // B), "s_dn")
+    _is(s_gu, _F32, (E, 2 * F // B, d // B), "s_gu")
+    _is(s_dn, _F32, (E, d // B, F // B), "s_dn")
     _on(w_gu, s_gu, w_dn, s_dn)
     return Experts(W_F8, E, d, F, w_gu.data_ptr(), s_gu.data_ptr(), None, w_dn.data_ptr(),
                    s_dn.data_ptr(), None, _ACT[act] if isinstance(act, str) else int(act))
@@ -397,18 +405,21 @@ def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUT
     T, d = xq.shape
     if d != experts.d:
         raise ValueError(f"xq is {list(xq.shape)}, the experts' d is {experts.d}")
-    _is(xs, torch.float32, (T, -(-d // FP8_BLOCK)), "xs")
-    R, F = T * k, experts.F
-    if rmap.numel() != R:
-        raise ValueError(f"the tables are of {rmap.numel()} rows, not {T} x {k}")
+    _is(xs, _F32, (T, -(-d // FP8_BLOCK)), "xs")
+    R, F, E = T * k, experts.F, experts.E
+    if rmap.numel() != R or roff.numel() != E + 1 or toff.numel() != E + 1:
+        raise ValueError(f"the tables are of {rmap.numel()} rows and {roff.numel() - 1} experts, "
+                         f"not {T} x {k} rows and {E}")
     ex = _f8_experts(experts)
-    hq = xq.new_empty((R, F), dtype=F8)
-    hs = xs.new_empty((R, -(-F // FP8_BLOCK)))
-    _check(lib.moe_grouped_swiglu_fp8(xq.data_ptr(), xs.data_ptr(), rmap.data_ptr(),
-                                      roff.data_ptr(), toff.data_ptr(), tables.BM, T, k,
-                                      ctypes.byref(ex), hq.data_ptr(), hs.data_ptr(), regime,
-                                      raw if stream is None else stream.cuda_stream),
-           "moe_grouped_swiglu_fp8")
+    dev = xq.device
+    hq = _empty(R, F, dtype=F8, device=dev)
+    hs = _empty(R, -(-F // FP8_BLOCK), dtype=_F32, device=dev)
+    st = lib.moe_grouped_swiglu_fp8(xq.data_ptr(), xs.data_ptr(), rmap.data_ptr(), roff.data_ptr(),
+                                    toff.data_ptr(), tables.BM, T, k, ctypes.byref(ex),
+                                    hq.data_ptr(), hs.data_ptr(), regime,
+                                    raw if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "moe_grouped_swiglu_fp8")
     return hq, hs
 
 
@@ -418,16 +429,20 @@ def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AU
     roff, toff = tables.row_off, tables.tile_off
     raw = _on(hq, hs, roff, toff)
     _codes(hq, 2, "hq")
-    R, F = T * k, experts.F
+    R, F, E = T * k, experts.F, experts.E
     if hq.shape != (R, F):
         raise ValueError(f"hq is {list(hq.shape)}, not [{T} x {k}, {F}]")
-    _is(hs, torch.float32, (R, -(-F // FP8_BLOCK)), "hs")
+    _is(hs, _F32, (R, -(-F // FP8_BLOCK)), "hs")
+    if tables.row_map.numel() != R or roff.numel() != E + 1 or toff.numel() != E + 1:
+        raise ValueError(f"the tables are of {tables.row_map.numel()} rows and "
+                         f"{roff.numel() - 1} experts, not {T} x {k} rows and {E}")
     ex = _f8_experts(experts)
-    ys = hs.new_empty((R, experts.d), dtype=torch.float16)
-    _check(lib.moe_grouped_down_fp8(hq.data_ptr(), hs.data_ptr(), roff.data_ptr(), toff.data_ptr(),
-                                    tables.BM, T, k, ctypes.byref(ex), ys.data_ptr(), regime,
-                                    raw if stream is None else stream.cuda_stream),
-           "moe_grouped_down_fp8")
+    ys = _empty(R, experts.d, dtype=torch.float16, device=hq.device)
+    st = lib.moe_grouped_down_fp8(hq.data_ptr(), hs.data_ptr(), roff.data_ptr(), toff.data_ptr(),
+                                  tables.BM, T, k, ctypes.byref(ex), ys.data_ptr(), regime,
+                                  raw if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "moe_grouped_down_fp8")
     return ys
 
 
@@ -442,14 +457,14 @@ class BalanceStats:
 
 
 def _balance_sizes(logits, mask, seq_off):
-    if logits.dtype != torch.float32 or logits.dim() != 2:
+    if logits.dtype != _F32 or logits.dim() != 2:
         raise ValueError(f"logits must be fp32 [T, E], got {logits.dtype} {list(logits.shape)}")
     T, E = logits.shape
-    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (T,)):
+    if mask is not None and (mask.dtype not in (torch.bool, _U8) or mask.shape != (T,)):
         raise ValueError(f"mask must be bool or uint8 [{T}], got {mask.dtype} {list(mask.shape)}")
     if seq_off is None:
         return T, E, 1
-    if seq_off.dtype != torch.int32 or seq_off.dim() != 1 or seq_off.numel() < 2:
+    if seq_off.dtype != _I32 or seq_off.dim() != 1 or seq_off.numel() < 2:
         raise ValueError("seq_off must be int32 [sequences + 1]")
     return T, E, seq_off.numel() - 1
 
@@ -463,25 +478,27 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
     moe_balance_loss_workspace bytes to reuse."""
     raw = _on(logits, topk_idx, mask, seq_off, ws)
     T, E, B = _balance_sizes(logits, mask, seq_off)
-    if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+    if topk_idx.dtype != _I32 or topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError(f"topk_idx must be int32 [{T}, k], got {topk_idx.dtype} "
                          f"{list(topk_idx.shape)}")
     k = topk_idx.shape[1]
-    loss = logits.new_empty(())
-    probs = logits.new_empty((B, E))
-    counts = topk_idx.new_empty((B, E))
-    tokens = topk_idx.new_empty((B,))
+    dev = logits.device
+    loss = torch.empty((), dtype=_F32, device=dev)
+    probs = _empty(B, E, dtype=_F32, device=dev)
+    counts = _empty(B, E, dtype=_I32, device=dev)
+    tokens = _empty(B, dtype=_I32, device=dev)
     if ws is None:
         need = lib.moe_balance_loss_workspace(T, E, B)
         if need:
-            ws = logits.new_empty((need,), dtype=torch.uint8)
+            ws = _empty(need, dtype=_U8, device=dev)
             if stream is not None:
                 ws.record_stream(stream)     # freed here, still in use there
-    _check(lib.moe_balance_loss(logits.data_ptr(), topk_idx.data_ptr(), _at(mask), _at(seq_off), T,
-                                E, k, B, coef, loss.data_ptr(), counts.data_ptr(),
-                                probs.data_ptr(), tokens.data_ptr(), _at(ws),
-                                0 if ws is None else ws.nbytes, raw if stream is None else stream.cuda_stream),
-           "moe_balance_loss")
+    st = lib.moe_balance_loss(logits.data_ptr(), topk_idx.data_ptr(), _at(mask), _at(seq_off), T, E,
+                              k, B, coef, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(),
+                              tokens.data_ptr(), _at(ws), 0 if ws is None else ws.nbytes,
+                              raw if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "moe_balance_loss")
     return BalanceStats(loss, counts, probs, tokens)
 
 
@@ -492,16 +509,16 @@ def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_o
     counts, tokens = stats.counts, stats.tokens
     raw = _on(logits, counts, tokens, mask, seq_off, dloss)
     T, E, B = _balance_sizes(logits, mask, seq_off)
-    _is(counts, torch.int32, (B, E), "stats.counts")
-    _is(tokens, torch.int32, (B,), "stats.tokens")
-    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+    _is(counts, _I32, (B, E), "stats.counts")
+    _is(tokens, _I32, (B,), "stats.tokens")
+    if dloss is not None and (dloss.dtype != _F32 or dloss.numel() != 1):
         raise ValueError("dloss must be one fp32 value")
     d = torch.empty_like(logits)
-    _check(lib.moe_balance_loss_backward(logits.data_ptr(), _at(mask), _at(seq_off), T, E, k, B,
-                                         coef, counts.data_ptr(), tokens.data_ptr(), _at(dloss),
-                                         d.data_ptr(),
-                                         raw if stream is None else stream.cuda_stream),
-           "moe_balance_loss_backward")
+    st = lib.moe_balance_loss_backward(logits.data_ptr(), _at(mask), _at(seq_off), T, E, k, B, coef,
+                                       counts.data_ptr(), tokens.data_ptr(), _at(dloss),
+                                       d.data_ptr(), raw if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "moe_balance_loss_backward")
     return d
 
 

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -178,10 +179,15 @@ inline bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// SMs of the current device (looked up once per device)
 inline int num_sms() {
+  static std::atomic<int> sms[64];
   int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return n;
+  const int known = sms[dev].load(std::memory_order_relaxed);
+  if (known) return known;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    sms[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
