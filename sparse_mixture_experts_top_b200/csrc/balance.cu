@@ -18,7 +18,8 @@
 // adds those in order: no floating-point atomics, so the same inputs give the
 // same bits. A sequence's chunks are consecutive, so the pair (chunk c,
 // sequence b) can own slot c + b: walking the tokens, each new pair raises c,
-// b or both. One chunk and one sequence need no second kernel.
+// b or both. A short single sequence is
+// one CTA's, with no second kernel.
 #include "common.cuh"
 #include "launch.h"
 
@@ -37,6 +38,11 @@ template <int LPR_, int NV_, int VEC_> struct Shape {
   static constexpr int LPR = LPR_, NV = NV_, VEC = VEC_, N = NV * VEC;
   static constexpr int TPW = 32 / LPR;                           // tokens of a warp at a time
   static constexpr int UN = N <= 8 ? 4 : N <= 16 ? 2 : 1;        // rows in flight per group
+  static constexpr int UF = UN > 1 ? UN / 2 : 1;                 // rows of a forward step
+  // warps of the CTA that takes a whole short sequence, and the tokens of its
+  // at most six steps (a second kernel and its workspace cost more)
+  static constexpr int SINGLE_WARPS = N <= 16 ? 16 : 8;
+  static constexpr int SINGLE_TOKENS = 6 * SINGLE_WARPS * TPW * UF;
 };
 
 // f(Shape) for rows of E logits
@@ -188,21 +194,23 @@ __device__ __forceinline__ float block_sum(float v, float* s_part) {
 }
 
 // One chunk of tokens: a partial row for each sequence that it meets. SINGLE:
-// the only chunk of the only sequence, whose sums are the result.
+// all tokens of the only sequence, whose sums are the result.
 template <typename S, bool SINGLE>
-__global__ void __launch_bounds__(kThreads) partial_kernel(const FwdParams p) {
+__global__ void __launch_bounds__(SINGLE ? S::SINGLE_WARPS * 32 : kThreads)
+    partial_kernel(const FwdParams p) {
+  constexpr int W = SINGLE ? S::SINGLE_WARPS : kWarps, THREADS = W * 32;
   extern __shared__ float sm[];
-  float* s_p = sm;                                             // [kWarps][E]
-  int* s_c = reinterpret_cast<int*>(sm + (size_t)kWarps * p.E);  // [E]
-  __shared__ int s_n[kWarps];
-  __shared__ float s_l[kWarps];
+  float* s_p = sm;                                        // [W][E]
+  int* s_c = reinterpret_cast<int*>(sm + (size_t)W * p.E);  // [E]
+  __shared__ int s_n[W];
+  __shared__ float s_l[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane / S::LPR, gl = lane % S::LPR;
-  constexpr int STEP = kWarps * S::TPW;
+  constexpr int STEP = W * S::TPW;
   pdl_wait();
   pdl_launch();
   if (!SINGLE && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;   // for the next kernel
-  const int t1 = (int)min((long long)p.T, (blockIdx.x + 1LL) * p.chunk);
+  const int t1 = SINGLE ? p.T : (int)min((long long)p.T, (blockIdx.x + 1LL) * p.chunk);
   for (int t0 = blockIdx.x * p.chunk; t0 < t1 || SINGLE;) {
     int end = t1, b = 0;
     if (t0 < t1) {
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) partial_kernel(const FwdParams p) {
         continue;
       }
     }
-    for (int e = threadIdx.x; e < p.E; e += kThreads) s_c[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += THREADS) s_c[e] = 0;
     __syncthreads();
     float acc[S::N];
 #pragma unroll
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) partial_kernel(const FwdParams p) {
     // The warp's tokens, UF per group and step (the same number of steps in all
     // its groups): while a step's rows are worked on, the next step's rows and
     // ids and the masks of the one behind it are on their way.
-    constexpr int UF = S::UN > 1 ? S::UN / 2 : 1;
+    constexpr int UF = S::UF;
     struct Step {
       Row<S> r[UF];
       int id[UF];
@@ -294,14 +302,14 @@ __global__ void __launch_bounds__(kThreads) partial_kernel(const FwdParams p) {
     __syncthreads();
     n = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) n += s_n[w];
+    for (int w = 0; w < W; ++w) n += s_n[w];
     const size_t slot = SINGLE ? 0 : (size_t)blockIdx.x + b;
     const float inv = n > 0 ? 1.f / (float)n : 0.f;
     float l = 0.f;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    for (int e = threadIdx.x; e < p.E; e += THREADS) {
       float v = s_p[e];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) v += s_p[w * p.E + e];
+      for (int w = 1; w < W; ++w) v += s_p[w * p.E + e];
       if constexpr (SINGLE) {
         p.probs[e] = v * inv;
         p.counts[e] = s_c[e];
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) partial_kernel(const FwdParams p) {
       }
     }
     if constexpr (SINGLE) {
-      l = block_sum<kWarps>(l, s_l);
+      l = block_sum<W>(l, s_l);
       if (threadIdx.x == 0) {
         *p.loss = p.factor * l;
         p.tokens[0] = n;
@@ -500,8 +508,10 @@ static Ws layout(int T, int E, int n_seq) {
 
 }  // namespace bal
 
-// one chunk and one sequence: no partial sums
-static bool single(int T, int E, int n_seq) { return n_seq == 1 && bal::chunks_of(T, E) <= 1; }
+// one sequence that one CTA takes: no partial sums
+static bool single(int T, int E, int n_seq) {
+  return n_seq == 1 && T <= bal::by_width(E, [](auto s) { return decltype(s)::SINGLE_TOKENS; });
+}
 
 size_t balance_workspace_bytes(int T, int E, int n_seq) {
   return single(T, E, n_seq) ? 0 : bal::layout(T, E, n_seq).total;
@@ -520,13 +530,14 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const u
                     (float*)(base + w.loss), (unsigned*)(base + w.counter),
                     loss, counts, probs, tokens};
   const bool one = single(T, E, n_seq);
-  const size_t smem = (size_t)(kWarps + 1) * E * 4;
   // at least one CTA, which clears the counter
   const unsigned grid = (unsigned)(p.n_chunks > 0 ? p.n_chunks : 1);
   const cudaError_t e = by_width(E, [&](auto shape) {
     using S = decltype(shape);
-    if (one) return launch_pdl(partial_kernel<S, true>, 1, kThreads, smem, s, p);
-    return launch_pdl(partial_kernel<S, false>, grid, kThreads, smem, s, p);
+    if (one)
+      return launch_pdl(partial_kernel<S, true>, 1, S::SINGLE_WARPS * 32,
+                        (size_t)(S::SINGLE_WARPS + 1) * E * 4, s, p);
+    return launch_pdl(partial_kernel<S, false>, grid, kThreads, (size_t)(kWarps + 1) * E * 4, s, p);
   });
   if (e != cudaSuccess || one) return e;
   return launch_pdl(finish_kernel, (unsigned)((E + 31) / 32) * (unsigned)n_seq, kFinishWarps * 32,
