@@ -591,19 +591,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = u0; u < total && ok; u += u_step) {
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
           const uint32_t s = it % C::NS, b = it % C::NBUF;
-          // buffer b was read back NBUF k-blocks ago
-          if (it >= (uint32_t)C::NBUF)
-            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
-                                p.status, true, p.wait_limit);
-          if (!ok) break;
           ok = mbar_wait_warp(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
                               p.wait_limit);
           if (ok && GLU)
             ok = mbar_wait_warp(smem_u32(rows_full + s), (it / C::NS) & 1, abort_flag, p.status,
                                 true, p.wait_limit);
-          if (!ok) break;
           // (the gathered rows were written by ordinary copies)
           if (GLU) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          // buffer b was read back NBUF k-blocks ago: waited for last, as the
+          // hand-over of the buffers sets the pace
+          if (ok && it >= (uint32_t)C::NBUF)
+            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
+                                p.status, true, p.wait_limit);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t off = s * kStage16;
           mma_block(tm + b * BN, alo0 + off, ahi, blo0 + off, bhi, idesc);
