@@ -77,7 +77,9 @@
  *   MOE_REGIME_AUTO: TC wherever the tensor-core kernels tile the shape
  *     (16-bit activations), except that moe_forward keeps the fused decode
  *     kernel while it applies and T*k < E; GEMV for everything else
- *     (f32 activations, other shapes).
+ *     (f32 activations, other shapes). MOE_W_F8 experts: TC except for a few
+ *     routed rows of small experts, gate|up and down each for itself (the
+ *     regime reported is gate|up's).
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
@@ -344,7 +346,10 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
  *   hq, hs   (device, out) e4m3 [T*k][F] and fp32 [T*k][F/128]:
  *            h = act(g) * u in fp32, quantised as moe_quantize_fp8 (block 1)
  *            does it
- * Regimes: as moe_grouped_swiglu (no fp16 range applies: every scale is fp32). */
+ * Regimes: MOE_REGIME_GEMV any BM; MOE_REGIME_TC BM = 128 (moe_sort_block_m());
+ * MOE_REGIME_AUTO the tensor cores where BM = 128, except for a few routed rows
+ * of small experts. Every shape with d and F multiples of 128 is taken by both.
+ * No fp16 range applies: every scale is fp32. */
 moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_t* row_map,
                                   const int32_t* row_off, const int32_t* tile_off, int BM, int T,
                                   int k, const moe_experts* experts, void* hq, float* hs,
@@ -353,7 +358,8 @@ moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_
 /* moe_grouped_down for MOE_W_F8 experts.
  *   hq, hs   (device) as moe_grouped_swiglu_fp8 writes them
  *   ys       (device, out) [T*k][d] fp16, as moe_grouped_down stores it for
- *            16-bit activations (moe_combine reads it) */
+ *            16-bit activations (moe_combine reads it; values outside the fp16
+ *            range are reported as MOE_ERR_RANGE in the device status) */
 moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* row_off,
                                 const int32_t* tile_off, int BM, int T, int k,
                                 const moe_experts* experts, void* ys, moe_regime regime,
@@ -377,7 +383,7 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
  *   seq_off  (device) int32 [n_seq+1], ascending in [0, T]: sequence b is the
  *            tokens seq_off[b] .. seq_off[b+1]-1; tokens outside all of them
  *            take no part. NULL: one sequence of all T tokens (n_seq = 1)
- *   n_seq    1 .. 65536
+ *   n_seq    1 .. 65536; T at most 2^30
  *   loss     (device, out) fp32 [1]
  *   counts   (device, out) int32 [n_seq][E]
  *   probs    (device, out) fp32 [n_seq][E]

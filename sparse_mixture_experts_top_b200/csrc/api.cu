@@ -442,11 +442,13 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
                            (cudaStream_t)stream));
 }
 
-// sequences of one balance loss at most (their partial sums are per sequence)
+// sequences of one balance loss at most (their partial sums are per sequence),
+// and tokens (whose numbers, with a CTA's step past the last, stay in 32 bits)
 static const int kMaxSeqs = 1 << 16;
+static const int kMaxTokens = 1 << 30;
 
 size_t moe_balance_loss_workspace(int T, int E, int n_seq) {
-  if (T < 0 || E <= 0 || E > 1024 || n_seq < 1) return 0;
+  if (T < 0 || T > kMaxTokens || E <= 0 || E > 1024 || n_seq < 1 || n_seq > kMaxSeqs) return 0;
   return balance_workspace_bytes(T, E, n_seq);
 }
 
@@ -454,7 +456,7 @@ static moe_status check_balance(const int32_t* seq_off, int T, int E, int k, int
   const moe_status st = check_dims(T, 64, E, k);
   if (st != MOE_OK) return st;
   if (n_seq < 1 || (!seq_off && n_seq != 1)) return MOE_ERR_INVALID_ARG;
-  return n_seq > kMaxSeqs ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return n_seq > kMaxSeqs || T > kMaxTokens ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
@@ -596,7 +598,9 @@ moe_status moe_forward_layout(int T, int d, int E, int k, int F, moe_dtype dt, m
   // fp16 token rows: x converted (weight-streaming), or permuted (the
   // one-launch path), or gathered in sorted row order (tensor cores)
   // (e4m3 experts: the token rows' codes and scales, in token order)
-  L.x16 = take(wfmt == MOE_W_F8 ? fp8_bytes(T, d) : dt == MOE_F32 ? 0 : (size_t)(L.regime == MOE_REGIME_TC ? R : T) * d * 2);
+  L.x16 = take(wfmt == MOE_W_F8 ? fp8_bytes(T, d)
+               : dt == MOE_F32  ? 0
+                                : (size_t)(L.regime == MOE_REGIME_TC ? R : T) * d * 2);
   L.total = off;
   *out = L;
   return MOE_OK;
@@ -629,7 +633,8 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
   // AUTO resolves to TC only for shapes and formats the tensor-core kernels
   // tile; an explicit TC request for others is refused
   const int regime_run = L.regime;
-  if (regime_run == MOE_REGIME_TC && experts->fmt != MOE_W_F8 && !tc_shape_supported(d, F, experts->fmt, dt))
+  if (regime_run == MOE_REGIME_TC && experts->fmt != MOE_W_F8 &&
+      !tc_shape_supported(d, F, experts->fmt, dt))
     return MOE_ERR_UNSUPPORTED;
 
   char* base = static_cast<char*>(ws);

@@ -29,7 +29,11 @@ namespace bal {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxChunks = 592;        // chunks of tokens at most: four CTAs for each of 148 SMs
-constexpr int kFinishWarps = 32;
+// the finishing kernel: experts of a CTA, and groups of its threads that share
+// out the chunks (a sequence's 592 chunks are nine loads deep)
+constexpr int kFinishE = 8;
+constexpr int kFinishGroups = 64;
+constexpr int kFinishThreads = kFinishE * kFinishGroups;
 
 // How a row of E logits lies in a lane group: LPR lanes, NV steps of VEC
 // consecutive logits each (VEC 4 where every row starts on a 16-byte
@@ -173,7 +177,7 @@ struct FwdParams {
   float* part_p;       // [n_chunks + n_seq][E]
   int32_t* part_c;     // [n_chunks + n_seq][E]
   int32_t* part_n;     // [n_chunks + n_seq]
-  float* part_loss;    // [n_seq * ceil(E / 32)]
+  float* part_loss;    // [n_seq * ceil(E / kFinishE)]
   unsigned* counter;
   float* loss;
   int32_t* counts;
@@ -333,20 +337,20 @@ __global__ void __launch_bounds__(SINGLE ? S::SINGLE_WARPS * 32 : kThreads)
   }
 }
 
-// 32 experts of one sequence per CTA: the warps add every 32nd chunk's partial
-// sums, then those in order. The last CTA to finish adds the CTAs' parts of
-// the loss, in order.
-__global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const FwdParams p) {
-  __shared__ float s_p[kFinishWarps][32];
-  __shared__ int s_c[kFinishWarps][32];
-  __shared__ int s_n[kFinishWarps];
-  __shared__ float s_l[kFinishWarps];
+// kFinishE experts of one sequence per CTA: group g of its threads adds the
+// partial sums of chunks g, g + kFinishGroups, ..., then the groups' are added
+// in order. The last CTA to finish adds the CTAs' parts of the loss, in order.
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FwdParams p) {
+  __shared__ float s_p[kFinishGroups][kFinishE];
+  __shared__ int s_c[kFinishGroups][kFinishE];
+  __shared__ int s_n[kFinishGroups];
+  __shared__ float s_l[kFinishThreads / 32];
   __shared__ bool s_last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int el = threadIdx.x % kFinishE, grp = threadIdx.x / kFinishE;
   pdl_wait();
   pdl_launch();
-  const int eb = (p.E + 31) / 32;
-  const int b = blockIdx.x / eb, e = (blockIdx.x % eb) * 32 + lane;
+  const int eb = (p.E + kFinishE - 1) / kFinishE;
+  const int b = blockIdx.x / eb, e = (blockIdx.x % eb) * kFinishE + el;
   int t0 = 0, t1 = p.T;
   if (p.off) {
     t0 = max(0, min(__ldg(p.off + b), p.T));
@@ -355,41 +359,60 @@ __global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const FwdPara
   float v = 0.f;
   int c = 0, n = 0;
   if (t0 < t1) {
-    const int c1 = (t1 - 1) / p.chunk;
-#pragma unroll 8
-    for (int i = t0 / p.chunk + warp; i <= c1; i += kFinishWarps) {
-      const size_t slot = (size_t)i + b;
-      if (e < p.E) {
-        v += p.part_p[slot * p.E + e];
-        c += p.part_c[slot * p.E + e];
+    const int c0 = t0 / p.chunk + grp, c1 = (t1 - 1) / p.chunk;
+    // four chunks at a time, whose loads go out together
+    for (int i = c0; i <= c1; i += 4 * kFinishGroups) {
+      float pv[4];
+      int pc[4], pn[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int ch = i + j * kFinishGroups;
+        const size_t slot = (size_t)ch + b;
+        const bool in = ch <= c1;
+        pv[j] = in && e < p.E ? p.part_p[slot * p.E + e] : 0.f;
+        pc[j] = in && e < p.E ? p.part_c[slot * p.E + e] : 0;
+        pn[j] = in ? p.part_n[slot] : 0;
       }
-      n += p.part_n[slot];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v += pv[j];
+        c += pc[j];
+        n += pn[j];
+      }
     }
   }
-  s_p[warp][lane] = v;
-  s_c[warp][lane] = c;
-  if (lane == 0) s_n[warp] = n;
+  s_p[grp][el] = v;
+  s_c[grp][el] = c;
+  if (el == 0) s_n[grp] = n;
   __syncthreads();
-  if (warp == 0) {
+  if (threadIdx.x < 32) {
+    // lane: expert el of quarter grp of the groups, then the quarters in order
+    constexpr int Q = kFinishGroups / 4;
     v = 0.f;
     c = 0;
     n = 0;
 #pragma unroll
-    for (int w = 0; w < kFinishWarps; ++w) {
-      v += s_p[w][lane];
-      c += s_c[w][lane];
-      n += s_n[w];
+    for (int g = 0; g < Q; ++g) {
+      v += s_p[grp * Q + g][el];
+      c += s_c[grp * Q + g][el];
+      n += s_n[grp * Q + g];
+    }
+#pragma unroll
+    for (int o = kFinishE; o < 32; o <<= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
     }
     const float inv = n > 0 ? 1.f / (float)n : 0.f;
     v *= inv;
-    if (e < p.E) {
+    float l = 0.f;
+    if (grp == 0 && e < p.E) {
       p.counts[(size_t)b * p.E + e] = c;
       p.probs[(size_t)b * p.E + e] = v;
-    } else {
-      v = 0.f;
+      l = (float)c * inv * v;
     }
-    const float l = warp_sum((float)c * inv * v);
-    if (lane == 0) {
+    l = warp_sum(l);
+    if (threadIdx.x == 0) {
       if (blockIdx.x % eb == 0) p.tokens[b] = n;
       p.part_loss[blockIdx.x] = l;
       __threadfence();
@@ -400,9 +423,8 @@ __global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const FwdPara
   if (!s_last) return;
   __threadfence();
   float l = 0.f;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinishWarps * 32)
-    l += __ldcg(p.part_loss + i);
-  l = block_sum<kFinishWarps>(l, s_l);
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinishThreads) l += __ldcg(p.part_loss + i);
+  l = block_sum<kFinishThreads / 32>(l, s_l);
   if (threadIdx.x == 0) *p.loss = p.factor * l;
 }
 
@@ -501,7 +523,7 @@ static Ws layout(int T, int E, int n_seq) {
   w.c = up(slots * E * 4);
   w.n = w.c + up(slots * E * 4);
   w.loss = w.n + up(slots * 4);
-  w.counter = w.loss + up((size_t)n_seq * ((E + 31) / 32) * 4);
+  w.counter = w.loss + up((size_t)n_seq * ((E + kFinishE - 1) / kFinishE) * 4);
   w.total = w.counter + 256;
   return w;
 }
@@ -540,8 +562,8 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const u
     return launch_pdl(partial_kernel<S, false>, grid, kThreads, (size_t)(kWarps + 1) * E * 4, s, p);
   });
   if (e != cudaSuccess || one) return e;
-  return launch_pdl(finish_kernel, (unsigned)((E + 31) / 32) * (unsigned)n_seq, kFinishWarps * 32,
-                    0, s, p);
+  return launch_pdl(finish_kernel, (unsigned)((E + kFinishE - 1) / kFinishE) * (unsigned)n_seq,
+                    kFinishThreads, 0, s, p);
 }
 
 cudaError_t launch_balance_loss_backward(const float* logits, const uint8_t* mask,

@@ -125,6 +125,7 @@ def test_calls_refuse_bad_arguments_without_launching(moe):
     assert f(T=9000, ws=P) == moe.ERR_WORKSPACE and f(T=9000, n=8) == moe.ERR_WORKSPACE
     assert f(T=9000, ws=odd) == moe.ERR_WORKSPACE and f(off=p, B=2, ws=P) == moe.ERR_WORKSPACE
     assert f(T=1 << 30, k=4) == UNS                   # T * k past 32 bits
+    assert f(T=(1 << 30) + 1, k=1) == UNS
     assert L.moe_balance_loss_workspace(-1, 8, 1) == 0
     assert L.moe_balance_loss_workspace(4, 8, 1) == 0 < L.moe_balance_loss_workspace(4, 8, 2)
 

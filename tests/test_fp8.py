@@ -328,7 +328,8 @@ def test_expert_stages_tensor_cores(moe, T, E, k, d, F, skew, act):
 
 
 @gpu
-def test_expert_stages_nan_rows_stay_their_own(moe):
+@pytest.mark.parametrize("regime", [1, 2])
+def test_expert_stages_nan_rows_stay_their_own(moe, regime):
     T, E, k, d, F = 6, 4, 2, 256, 128
     ex = _experts(E, d, F, 3)
     idx = mi.random_topk_idx(T, E, k, 3).to(DEV)
@@ -336,11 +337,42 @@ def test_expert_stages_nan_rows_stay_their_own(moe):
     x = torch.randn(T, d, device=DEV)
     x[4, 9] = float("inf")
     xq, xs = moe.quantize_fp8(x)
-    hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, k, ex)
+    hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, k, ex, regime)
     bad = (st.row_map.view(torch.int32) == 4).cpu().numpy()
     H = values(hq)
     assert np.isnan(H[bad]).all() and np.isfinite(H[~bad]).all()
     assert np.isfinite(hs.cpu().numpy()).all()
+    ys = moe.grouped_down_fp8(hq, hs, st, T, k, ex, regime).cpu().numpy()
+    assert np.isnan(ys[bad]).all() and np.isfinite(ys[~bad]).all()
+    assert moe.device_status() == moe.ERR_RANGE          # as any ys that is not finite
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(20, 512, 384), (900, 2048, 256)])
+def test_results_at_any_16_byte_boundary(moe, M, N, K):
+    """An output that starts 16 but not 32 bytes into an allocation, for the
+    split and the persistent tensor-core form; nothing beside it is written."""
+    a, sa, b, sb = _operands(moe, M, N, K, 9)
+    buf = torch.full((M * N + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = moe.fp8_matmul(a, sa, b, sb, out=buf[8:8 + M * N].view(M, N))
+    _check_matmul(y, a, sa, b, sb, torch.bfloat16)
+    assert (buf[:8] == 7).all() and (buf[8 + M * N:] == 7).all()
+    # gate|up codes through the C call
+    T, E, k, d, F = 700, 4, 2, 256, 2048
+    ex = _experts(E, d, F, 1)
+    idx = mi.random_topk_idx(T, E, k, 1).to(DEV)
+    st = moe.sort_rows(idx, E, 128)
+    xq, xs = moe.quantize_fp8(torch.randn(T, d, device=DEV))
+    hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, k, ex, moe.REGIME_TC)
+    h2 = torch.full((T * k * F + 32,), 9, dtype=torch.uint8, device=DEV)
+    s2 = torch.empty_like(hs)
+    e = moe.experts_struct(ex)
+    assert moe.lib.moe_grouped_swiglu_fp8(
+        xq.data_ptr(), xs.data_ptr(), st.row_map.data_ptr(), st.row_off.data_ptr(),
+        st.tile_off.data_ptr(), 128, T, k, ctypes.byref(e), h2.data_ptr() + 16, s2.data_ptr(),
+        moe.REGIME_TC, torch.cuda.current_stream().cuda_stream) == moe.OK
+    assert torch.equal(h2[16:-16], hq.view(torch.uint8).flatten()) and torch.equal(s2, hs)
+    assert (h2[:16] == 9).all() and (h2[-16:] == 9).all()
 
 
 @gpu
