@@ -435,6 +435,36 @@ def test_same_bits_every_time(moe):
             assert torch.equal(moe.grouped_down_fp8(hq, hs, st, 500, 4, ex, rg), ys)
 
 
+@gpu
+def test_two_streams_at_once(moe):
+    """The same calls on two streams that overlap give the bits of one."""
+    a, sa, b, sb = _operands(moe, 200, 1024, 2048, 4)
+    ex = _experts(16, 512, 256, 8)
+    idx = mi.random_topk_idx(64, 16, 4, 2).to(DEV)
+    st = moe.sort_rows(idx, 16, 128)
+    x = torch.randn(64, 512, device=DEV)
+
+    def step(stream=None):
+        xq, xs = moe.quantize_fp8(x, stream=stream)
+        hq, hs = moe.grouped_swiglu_fp8(xq, xs, st, 4, ex, stream=stream)
+        return [moe.fp8_matmul(a, sa, b, sb, stream=stream), xq, xs, hq, hs,
+                moe.grouped_down_fp8(hq, hs, st, 64, 4, ex, stream=stream)]
+
+    ref = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                out.append(step())
+            out.append(step(s))
+    torch.cuda.synchronize()
+    for o in out:
+        for g, w in zip(o, ref):
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
+
+
 # ------------------------------------------------------------------ whole layer
 
 @gpu
@@ -445,6 +475,13 @@ def test_forward_with_f8_experts(moe, T, E, k, d, F, act):
     and near the 64-bit layer of the same quantised operands."""
     wl = mi.Workload("f8", T, d, E, k, F, act, "f8", "normal0.5")
     L = mi.make_layer(wl, 1, DEV)
+    if E == 8:            # experts quantised by the library from bf16 weights, packed from gate and up
+        g = torch.Generator(device=DEV).manual_seed(5)
+        mk = lambda n, m: (torch.randn(E, n, m, generator=g, device=DEV) / m ** 0.5).bfloat16()  # noqa: E731
+        (wg, sg), (wu, su), (wd, sd) = (moe.quantize_fp8(mk(n, m), 128)
+                                        for n, m in ((F, d), (F, d), (d, F)))
+        w_gu, s_gu, _ = moe.pack_gate_up("f8", wg, wu, s_g=sg, s_u=su)
+        L.experts = mi.Experts("f8", E, d, F, w_gu, wd, s_gu, None, sd, None)
     y = moe.forward(L.x, L.w_router, L.router_bias, L.experts, k)
     lay = moe.forward_layout(T, d, E, k, F, L.x.dtype, "f8")
     logits, idx, w = moe.route(L.x, L.w_router, L.router_bias, k)
