@@ -656,32 +656,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p.wait_limit);
         if (!ok) break;
         tc_fence_after();
-        // a chunk of 16 columns is scaled while the next is on its way; the
-        // buffer is handed back as soon as the last has arrived
+        // 16 columns at a time (the two warps of a scheduler hide each other's
+        // reads); the buffer is handed back as soon as the last have arrived
         constexpr int NCH = COLS / 16, H = COLS / 2;
-        uint32_t d[2][16];
+        auto hand_back = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
+        };
         if (live) {
-          tmem_ld_start(tl + b * BN + c0, d[0]);
-          tmem_ld_wait(d[0]);
-        }
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          if (live && j + 1 < NCH) {
-            const int c = (j + 1) * 16;
-            tmem_ld_start(tl + b * BN + (c < H ? c0 + c : c1 + c - H), d[(j + 1) & 1]);
-          }
-          if (j + 1 == NCH) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
-          }
-          if (live) {
-            const float f = j * 16 < H ? f0 : f1;
+          for (int j = 0; j < NCH; ++j) {
+            const int c = j * 16;
+            uint32_t d[16];
+            tmem_ld_start(tl + b * BN + (c < H ? c0 + c : c1 + c - H), d);
+            tmem_ld_wait(d);
+            if (j + 1 == NCH) hand_back();
+            const float f = c < H ? f0 : f1;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              fma2(acc[j * 16 + i], acc[j * 16 + i + 1], d[j & 1][i], d[j & 1][i + 1], f);
-            if (j + 1 < NCH) tmem_ld_wait(d[(j + 1) & 1]);
+            for (int i = 0; i < 16; i += 2) fma2(acc[c + i], acc[c + i + 1], d[i], d[i + 1], f);
           }
+        } else {
+          hand_back();
         }
       }
       if (!ok) break;
