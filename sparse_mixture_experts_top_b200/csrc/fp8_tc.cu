@@ -33,6 +33,16 @@
 //     stores them: all SMs stream weights, and the result stays the same from
 //     run to run.
 //
+// What bounds it, on one B200: many rows, the hand-over of the two accumulator
+// buffers and the clock under the power cap (4096 x 4096 x 7168: 119 us in a
+// burst, 138 us sustained, 0.61 and 0.53 of twice the measured bf16 rate; the
+// same loop without loads and stores runs at 565 cycles a k-block, the MMAs
+// alone at 512); few rows, the weights' bytes (down of 256 rows over 128 experts
+// 28 us, 0.97 of the measured HBM rate; gate|up of 20,480 rows over 512 experts
+// 216 us, 0.77). A pair of CTAs on one tile (cta_group::2) moves a third less
+// through shared memory but hands buffers over between SMs: 2 % faster, not
+// kept; MMAs of N = 128 with four buffers read the token rows twice: slower.
+//
 // Every mbarrier wait is bounded, as in the other tensor-core kernels; the
 // cluster barriers are reached by every thread, whatever the waits did.
 #include <cooperative_groups.h>
