@@ -20,8 +20,9 @@
 // sequence b) can own slot c + b: walking the tokens, each new pair raises c,
 // b or both. A short single sequence is
 // one CTA's, with no second kernel. 65521 x 256 logits in 13 masked sequences
-// take 24 us forward (0.42 of the measured HBM rate; the second kernel's chain of
-// loads is 5 of them) and 27 us backward (0.77) on one B200.
+// take 24 us forward (0.43 of the measured HBM rate; the second kernel takes 8 us
+// when it runs alone, from the latency of its loads) and 28 us backward (0.72) on
+// one B200.
 #include "common.cuh"
 #include "launch.h"
 

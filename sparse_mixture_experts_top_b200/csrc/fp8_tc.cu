@@ -13,7 +13,8 @@
 // xs[m][kb] ws[.][kb] is one value per thread and 64 columns: one FMA per element.
 //
 // Warps: 0 loads by TMA (a stage's weight rows in one copy, its token rows in
-// another: every further copy of a stage cost about 65 cycles), 1 issues the
+// another: with the token rows in four copies the product below took 147 instead
+// of 123 us, about 65 cycles a copy), 1 issues the
 // MMAs, 2 and 3 gather token rows through row_map (16-byte asynchronous copies
 // into the same swizzled layout; TMA's four-row gathers were slower), 4..11
 // scale, add and store: warp w reads TMEM lanes 32 (w % 4) .., and half (w - 4) / 4 of the
@@ -35,13 +36,13 @@
 //
 // What bounds it, on one B200: many rows, the hand-over of the two accumulator
 // buffers and the clock under the power cap (4096 x 4096 x 7168: 119 us in a
-// burst, 138 us sustained, 0.61 and 0.53 of twice the measured bf16 rate; the
-// same loop without loads and stores runs at 565 cycles a k-block, the MMAs
-// alone at 512); few rows, the weights' bytes (down of 256 rows over 128 experts
+// burst, 138 us sustained, 0.61 and 0.53 of twice the measured bf16 rate; an
+// MMA with its commit, read-back and scaling, operands resident, takes 563 cycles
+// a k-block, the MMAs alone 512); few rows, the weights' bytes (down of 256 rows over 128 experts
 // 28 us, 0.97 of the measured HBM rate; gate|up of 20,480 rows over 512 experts
 // 216 us, 0.77). A pair of CTAs on one tile (cta_group::2) moves a third less
-// through shared memory but hands buffers over between SMs: 2 % faster, not
-// kept; MMAs of N = 128 with four buffers read the token rows twice: slower.
+// through shared memory but hands buffers over between SMs: 145 against 149 us
+// sustained, not kept; MMAs of N = 128 with four buffers read the token rows twice: slower.
 //
 // Every mbarrier wait is bounded, as in the other tensor-core kernels; the
 // cluster barriers are reached by every thread, whatever the waits did.
