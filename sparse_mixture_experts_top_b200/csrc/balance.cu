@@ -504,8 +504,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdParams p) {
         float d[S::VEC];
 #pragma unroll
         for (int j = 0; j < S::VEC; ++j)
-          // (a token of no sequence is zero whatever its logits hold)
-          d[j] = b >= 0 ? r[u].v[i * S::VEC + j] * z * (a[i * S::VEC + j] - s) : 0.f;
+          // (a token that takes no part is zero whatever its logits and dloss hold)
+          d[j] = b >= 0 && ok[u] ? r[u].v[i * S::VEC + j] * z * (a[i * S::VEC + j] - s) : 0.f;
         if constexpr (S::VEC == 4)
           *reinterpret_cast<float4*>(out + e) = make_float4(d[0], d[1], d[2], d[3]);
         else

@@ -256,6 +256,22 @@ def test_same_bits_in_a_graph_and_with_a_shared_workspace(moe):
 
 
 @gpu
+@pytest.mark.parametrize("dloss", [float("inf"), float("nan")])
+@pytest.mark.parametrize("E", [8, 33, 256])
+def test_a_gradient_that_is_not_finite_stays_with_its_tokens(moe, E, dloss):
+    """A loss scaled past the fp32 range: tokens that take no part keep a zero
+    gradient, the others show it."""
+    lg, idx, mask, off = (t.to(DEV) for t in inputs(90, E, 2, E, 3, True))
+    st = moe.balance_loss(lg, idx, 1.0, mask, off)
+    d = moe.balance_loss_backward(lg, st, 2, 1.0, mask, off,
+                                  dloss=torch.tensor(dloss, device=DEV))
+    t = torch.arange(90, device=DEV)
+    part = mask & (t >= off[0]) & (t < off[-1])
+    assert 0 < part.sum() < 90
+    assert (d[~part] == 0).all() and not torch.isfinite(d[part]).all(1).any()
+
+
+@gpu
 def test_binding_refusals(moe):
     lg, idx, mask, off = (None if t is None else t.to(DEV) for t in inputs(10, 8, 2, 1, 2, True))
     for bad in (dict(logits=lg.double()), dict(topk_idx=idx.long()), dict(topk_idx=idx[:5]),
