@@ -320,8 +320,8 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
  *         row counts are multiples of 128 may be given as one)
  *   q     (device, out) e4m3 [rows][K]
  *   s     (device, out) fp32
- * The last block of a row (or of the rows) may be partial. rows = 0 returns
- * MOE_OK and launches nothing. */
+ * rows and K are at most 2^30. The last block of a row (or of the rows) may be
+ * partial. rows = 0 returns MOE_OK and launches nothing. */
 moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int block, void* q,
                             float* s, moe_stream_t stream);
 
@@ -333,7 +333,7 @@ moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int bl
  *   y  (device, out) [M][N], dtype dt; fp32 sums, rounded once. MOE_F16: values
  *      outside the fp16 range are reported as MOE_ERR_RANGE in the device
  *      status
- * K is a multiple of 16; M and N are any sizes. M = 0 returns MOE_OK and
+ * K is a multiple of 16; M and N are any sizes; each at most 2^30. M = 0 returns MOE_OK and
  * launches nothing. */
 moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int M,
                           int N, int K, moe_dtype dt, void* y, moe_stream_t stream);

@@ -319,6 +319,12 @@ def _codes(t, dims, what):
         raise ValueError(f"{what} must have {dims} dimensions, got {list(t.shape)}")
 
 
+def _sizes(*ns):
+    """The library's size limit, which a larger Python int would slip past as a C int."""
+    if max(ns) > 1 << 30:
+        raise ValueError(f"sizes {list(ns)}: rows, columns and tokens are limited to 2^30 each")
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -337,6 +343,9 @@ def quantize_fp8(x, block=1, stream=None):
     if block != 1 and block != FP8_BLOCK:
         raise ValueError(f"block must be 1 or {FP8_BLOCK}, got {block}")
     n, groups = rows, (rows if block == 1 else -(-rows // FP8_BLOCK))
+    if len(shape) > 2:
+        n = x.numel() // K if K else 0
+    _sizes(n, K)
     q = torch.empty_like(x, dtype=F8)
     if len(shape) == 2:
         s = _empty(groups, -(-K // FP8_BLOCK), dtype=_F32, device=x.device)
@@ -344,7 +353,6 @@ def quantize_fp8(x, block=1, stream=None):
         if block != 1 and rows % FP8_BLOCK:
             raise ValueError("a stack of weights needs rows in multiples of 128 (a block of "
                              "scales may not straddle two of them)")
-        n = x.numel() // K if K else 0
         s = _empty(*shape[:-2], groups, -(-K // FP8_BLOCK), dtype=_F32, device=x.device)
     st = lib.moe_quantize_fp8(x.data_ptr(), _dt(x), n, K, block, q.data_ptr(), s.data_ptr(),
                               raw if stream is None else stream.cuda_stream)
@@ -363,6 +371,7 @@ def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
     N, Kb = b.shape
     if Kb != K:
         raise ValueError(f"a is [{M}, {K}] and b [{N}, {Kb}]: K differs")
+    _sizes(M, N, K)
     KB = -(-K // FP8_BLOCK)
     _is(sa, _F32, (M, KB), "sa")
     _is(sb, _F32, (-(-N // FP8_BLOCK), KB), "sb")
@@ -460,6 +469,7 @@ def _balance_sizes(logits, mask, seq_off):
     if logits.dtype != _F32 or logits.dim() != 2:
         raise ValueError(f"logits must be fp32 [T, E], got {logits.dtype} {list(logits.shape)}")
     T, E = logits.shape
+    _sizes(T)
     if mask is not None and (mask.dtype not in (torch.bool, _U8) or mask.shape != (T,)):
         raise ValueError(f"mask must be bool or uint8 [{T}], got {mask.dtype} {list(mask.shape)}")
     if seq_off is None:

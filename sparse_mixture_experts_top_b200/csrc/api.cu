@@ -373,11 +373,15 @@ moe_status moe_grouped_down(const void* h, moe_dtype dt, const int32_t* row_off,
   return launched(down_gemv(h, dt, row_off, tile_off, BM, (int)R, *experts, ys, status_ptr(), s));
 }
 
+// rows, columns and tokens of the fp8 and balance calls at most: their numbers,
+// with a tile's or a CTA's step past the last, stay in 32 bits
+static const int kMaxSize = 1 << 30;
+
 moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int block, void* q,
                             float* s, moe_stream_t stream) {
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
   if (rows < 0 || K <= 0 || (block != 1 && block != 128)) return MOE_ERR_INVALID_ARG;
-  if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if (K % 16 || rows > kMaxSize || K > kMaxSize) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !q || !s) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return MOE_ERR_INVALID_ARG;
@@ -388,7 +392,7 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
                           int N, int K, moe_dtype dt, void* y, moe_stream_t stream) {
   if (!valid_dt(dt)) return MOE_ERR_INVALID_ARG;
   if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-  if (K % 16) return MOE_ERR_UNSUPPORTED;
+  if (K % 16 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!a || !sa || !b || !sb || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
@@ -442,13 +446,11 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
                            (cudaStream_t)stream));
 }
 
-// sequences of one balance loss at most (their partial sums are per sequence),
-// and tokens (whose numbers, with a CTA's step past the last, stay in 32 bits)
+// sequences of one balance loss at most (their partial sums are per sequence)
 static const int kMaxSeqs = 1 << 16;
-static const int kMaxTokens = 1 << 30;
 
 size_t moe_balance_loss_workspace(int T, int E, int n_seq) {
-  if (T < 0 || T > kMaxTokens || E <= 0 || E > 1024 || n_seq < 1 || n_seq > kMaxSeqs) return 0;
+  if (T < 0 || T > kMaxSize || E <= 0 || E > 1024 || n_seq < 1 || n_seq > kMaxSeqs) return 0;
   return balance_workspace_bytes(T, E, n_seq);
 }
 
@@ -456,7 +458,7 @@ static moe_status check_balance(const int32_t* seq_off, int T, int E, int k, int
   const moe_status st = check_dims(T, 64, E, k);
   if (st != MOE_OK) return st;
   if (n_seq < 1 || (!seq_off && n_seq != 1)) return MOE_ERR_INVALID_ARG;
-  return n_seq > kMaxSeqs || T > kMaxTokens ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return n_seq > kMaxSeqs || T > kMaxSize ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
@@ -679,7 +681,8 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
                         stp, s)) !=
         cudaSuccess)
       return launched(e);
-    if ((e = down_fp8(resolve_fp8(regime, R, E, d), h, hs, roff, toff, L.BM, (int)R, *experts, ys, stp, s)) != cudaSuccess)
+    if ((e = down_fp8(resolve_fp8(regime, R, E, d), h, hs, roff, toff, L.BM, (int)R, *experts, ys,
+                      stp, s)) != cudaSuccess)
       return launched(e);
   } else if (regime_run == MOE_REGIME_TC) {
     // h stays in the q4 dequant's permuted K order between the two kernels

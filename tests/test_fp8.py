@@ -60,6 +60,13 @@ def test_calls_refuse_bad_arguments_without_launching(moe):
     assert m(p, p, p, p, 4, 8, 128, moe.BF16, odd, P) == ARG
     assert m(p, p, p, p, 4, 8, 100, moe.BF16, p, P) == UNS
     assert m(P, P, P, P, 0, 8, 128, moe.BF16, P, P) == OK
+    big = (1 << 30) + 16                    # a tile past it would leave 32-bit indices
+    assert q(p, moe.BF16, big, 16, 128, p, p, P) == UNS
+    assert q(p, moe.BF16, 4, big, 1, p, p, P) == UNS
+    assert q(p, moe.BF16, 0x7fffffff, 16, 128, p, p, P) == UNS
+    assert m(p, p, p, p, big, 8, 16, moe.BF16, p, P) == UNS
+    assert m(p, p, p, p, 4, big, 16, moe.BF16, p, P) == UNS
+    assert m(p, p, p, p, 4, 8, big, moe.BF16, p, P) == UNS
 
     def ex(fmt=moe.W_F8, E=8, d=256, F=128, w=0x10000, s=0x10000):
         return ctypes.byref(moe.Experts(fmt, E, d, F, w, s, None, w, s, None))
@@ -106,6 +113,26 @@ def test_binding_refuses_bad_tensors(moe):
         moe.quantize_fp8(torch.zeros(4, 128))                     # not on the GPU
     with pytest.raises(ValueError):
         moe.fp8_matmul(*[torch.zeros(4, 128)] * 4)
+
+
+@pytest.mark.parametrize("rows", [(1 << 30) + 1, 1 << 31, (1 << 32) + 4])
+def test_binding_refuses_sizes_past_its_integers(moe, monkeypatch, rows):
+    """A size that a C int cannot hold is refused, not cut to its low bits.
+    (Meta tensors have such sizes without memory; the device check is passed over.)"""
+    monkeypatch.setattr(moe, "_on", lambda *ts: 0)
+    x = torch.empty(rows, 16, dtype=torch.bfloat16, device="meta")
+    a = torch.empty(rows, 16, dtype=torch.uint8, device="meta")
+    sa = torch.empty(rows, 1, device="meta")
+    b, sb = a[:8], sa[:1]
+    for call in (lambda: moe.quantize_fp8(x), lambda: moe.quantize_fp8(x, 128),
+                 lambda: moe.quantize_fp8(x.view(1, rows, 16)),
+                 lambda: moe.fp8_matmul(a, sa, b, sb),
+                 lambda: moe.fp8_matmul(b, sa[:8], a, sa[:-(-rows // 128)])):
+        with pytest.raises(ValueError, match="2\\^30"):
+            call()
+    idx = torch.empty(rows, 1, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="2\\^30"):
+        moe.balance_loss(x.float(), idx, 1.0)
 
 
 # ------------------------------------------------------------------ quantiser
