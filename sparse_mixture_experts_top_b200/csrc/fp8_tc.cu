@@ -36,7 +36,7 @@
 //
 // What bounds it, on one B200: many rows, the hand-over of the two accumulator
 // buffers and the clock under the power cap (4096 x 4096 x 7168: 119 us in a
-// burst, 138 us sustained, 0.61 and 0.53 of twice the measured bf16 rate; an
+// burst, 137 us sustained, 0.61 and 0.53 of twice the measured bf16 rate; an
 // MMA with its commit, read-back and scaling, operands resident, takes 563 cycles
 // a k-block, the MMAs alone 512); few rows, the weights' bytes (down of 256 rows over 128 experts
 // 28 us, 0.97 of the measured HBM rate; gate|up of 20,480 rows over 512 experts
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
             const uint32_t s = it % C::NS;
             if (it >= (uint32_t)C::NS) {
-              ok = mbar_wait(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
+              ok = mbar_wait<true>(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
                              true, p.wait_limit);
               if (!ok) break;
             }
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
           const uint32_t last = it - 1 - i;
-          mbar_wait(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status, false);
+          mbar_wait<true>(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status, false);
         }
       }
       __syncwarp();
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
           const uint32_t s = it % C::NS;
           if (it >= (uint32_t)C::NS) {
-            ok = mbar_wait_warp(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
+            ok = mbar_wait_warp<true>(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
                                 true, p.wait_limit);
             if (!ok) break;
           }
@@ -602,17 +602,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = u0; u < total && ok; u += u_step) {
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
           const uint32_t s = it % C::NS, b = it % C::NBUF;
-          ok = mbar_wait_warp(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
+          ok = mbar_wait_warp<true>(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
                               p.wait_limit);
           if (ok && GLU)
-            ok = mbar_wait_warp(smem_u32(rows_full + s), (it / C::NS) & 1, abort_flag, p.status,
+            ok = mbar_wait_warp<true>(smem_u32(rows_full + s), (it / C::NS) & 1, abort_flag, p.status,
                                 true, p.wait_limit);
           // (the gathered rows were written by ordinary copies)
           if (GLU) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           // buffer b was read back NBUF k-blocks ago: waited for last, as the
           // hand-over of the buffers sets the pace
           if (ok && it >= (uint32_t)C::NBUF)
-            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
+            ok = mbar_wait_warp<true>(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
                                 p.status, true, p.wait_limit);
           if (!ok) break;
           tc_fence_after();
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit_warp(smem_u32(drain));
-      mbar_wait_warp(smem_u32(drain), 0, abort_flag, p.status, false);
+      mbar_wait_warp<true>(smem_u32(drain), 0, abort_flag, p.status, false);
     }
     if constexpr (SPLIT) {
       cooperative_groups::this_cluster().sync();     // the two barriers of the joining warps
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (GLU) t.b1 = __ldg(++t.w1);
         }
         const uint32_t b = it % C::NBUF;
-        ok = mbar_wait_warp(smem_u32(acc_full + b), (it / C::NBUF) & 1, abort_flag, p.status, true,
+        ok = mbar_wait_warp<true>(smem_u32(acc_full + b), (it / C::NBUF) & 1, abort_flag, p.status, true,
                             p.wait_limit);
         if (!ok) break;
         tc_fence_after();
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         am[half * BM + m] = mx;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(xchg));
-        ok = mbar_wait_warp(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
+        ok = mbar_wait_warp<true>(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
         if (!ok) break;
         if (m < nv) {
           mx = fmaxf(am[m], am[BM + m]);

@@ -75,17 +75,24 @@ __device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity, ui
 // launch's bound (Params::wait_limit); the waits for copies and MMAs still in
 // flight before the CTA exits keep the full bound, so that nothing lands in
 // shared memory or TMEM after the CTA has released it. A bound below ~50 us
-// polls instead of suspending the thread, so the wait notices its deadline
-// promptly.
+// also drops the sleep hint, so the wait notices its deadline promptly; with
+// POLL such a bound never suspends the thread at all, so that a phase which is
+// not complete at once runs out for certain (a template argument: the choice at
+// every wait cost the grouped kernels 2 %).
+template <bool POLL = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int* status, bool honor_abort = true,
                                           long long limit = kWaitCycles) {
-  const bool sleep = limit >= 100000;
-  if (sleep ? mbar_try(bar, parity) : mbar_test(bar, parity)) return true;
+  const bool poll = POLL && limit < 100000;
+  if (poll ? mbar_test(bar, parity) : mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
+  const bool sleep = limit >= 100000;
   const uint32_t af = smem_u32(const_cast<const int*>(abort_flag));
   for (;;) {
-    if (sleep ? mbar_try_sleep(bar, parity, 20000u) : mbar_test(bar, parity)) return true;
+    if (sleep  ? mbar_try_sleep(bar, parity, 20000u)
+        : POLL ? mbar_test(bar, parity)
+               : mbar_try(bar, parity))
+      return true;
     uint32_t aborting;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(aborting) : "r"(af) : "memory");
     if (honor_abort && aborting) return false;
@@ -99,11 +106,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 
 // Every lane waits; the result is the same in all lanes, so the warp stays
 // converged for the .sync.aligned tcgen05 instructions that follow.
+template <bool POLL = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
                                                volatile int* abort_flag, int* status,
                                                bool honor_abort = true,
                                                long long limit = kWaitCycles) {
-  const bool r = mbar_wait(bar, parity, abort_flag, status, honor_abort, limit);
+  const bool r = mbar_wait<POLL>(bar, parity, abort_flag, status, honor_abort, limit);
   return __all_sync(0xffffffffu, r);
 }
 
