@@ -18,8 +18,10 @@
 // MMAs, 2 and 3 gather token rows through row_map (16-byte asynchronous copies
 // into the same swizzled layout; TMA's four-row gathers were slower), 4..11
 // scale, add and store: warp w reads TMEM lanes 32 (w % 4) .., and half (w - 4) / 4 of the
-// columns. Register shares: 72 per thread for warps 0..3, 216 for warps 4..11
-// (their sums of up to 128 columns live in registers), 168 at launch.
+// columns. Register shares: 88 per thread for warps 0..3, 208 for warps 4..11
+// (their sums of up to 128 columns live in registers), 168 at launch: 128 x 88 +
+// 256 x 208 = 384 x 168. With 72 and 216 the gathering warps spilled (gate|up of
+// 20,480 rows over 512 experts 264 against 246 us sustained).
 //
 // gate|up: the unit's weight rows are 128 gate and the 128 up rows of the same
 // features, so a thread holds both for 64 features; the GLU's result is
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb_hi = SPLIT ? (int)((long long)p.KB * (rank + 1) / p.split) : p.KB;
 
   if (warp < kAccWarp0) {
-    regs_dec<72>();
+    regs_dec<88>();
     if (warp == 0) {
       // ---------------------------------------------------------- loads (TMA)
       uint32_t it = 0;
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
             const uint32_t s = it % C::NS;
             if (it >= (uint32_t)C::NS) {
-              ok = mbar_wait<true>(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
+              ok = mbar_wait(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
                              true, p.wait_limit);
               if (!ok) break;
             }
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t i = 0; i < (uint32_t)C::NS && i < it; ++i) {
           const uint32_t last = it - 1 - i;
-          mbar_wait<true>(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status, false);
+          mbar_wait(smem_u32(full + last % C::NS), (last / C::NS) & 1, abort_flag, p.status, false);
         }
       }
       __syncwarp();
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
           const uint32_t s = it % C::NS;
           if (it >= (uint32_t)C::NS) {
-            ok = mbar_wait_warp<true>(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
+            ok = mbar_wait_warp(smem_u32(empty + s), ((it / C::NS) - 1) & 1, abort_flag, p.status,
                                 true, p.wait_limit);
             if (!ok) break;
           }
@@ -602,17 +604,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = u0; u < total && ok; u += u_step) {
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
           const uint32_t s = it % C::NS, b = it % C::NBUF;
-          ok = mbar_wait_warp<true>(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status, true,
-                              p.wait_limit);
+          // (its first wait is never met at once, so a short bound runs out here)
+          ok = mbar_wait_warp<true>(smem_u32(full + s), (it / C::NS) & 1, abort_flag, p.status,
+                                    true, p.wait_limit);
           if (ok && GLU)
-            ok = mbar_wait_warp<true>(smem_u32(rows_full + s), (it / C::NS) & 1, abort_flag, p.status,
+            ok = mbar_wait_warp(smem_u32(rows_full + s), (it / C::NS) & 1, abort_flag, p.status,
                                 true, p.wait_limit);
           // (the gathered rows were written by ordinary copies)
           if (GLU) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           // buffer b was read back NBUF k-blocks ago: waited for last, as the
           // hand-over of the buffers sets the pace
           if (ok && it >= (uint32_t)C::NBUF)
-            ok = mbar_wait_warp<true>(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
+            ok = mbar_wait_warp(smem_u32(acc_empty + b), ((it / C::NBUF) - 1) & 1, abort_flag,
                                 p.status, true, p.wait_limit);
           if (!ok) break;
           tc_fence_after();
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit_warp(smem_u32(drain));
-      mbar_wait_warp<true>(smem_u32(drain), 0, abort_flag, p.status, false);
+      mbar_wait_warp(smem_u32(drain), 0, abort_flag, p.status, false);
     }
     if constexpr (SPLIT) {
       cooperative_groups::this_cluster().sync();     // the two barriers of the joining warps
@@ -631,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ scale, add, store
-    regs_inc<216>();
+    regs_inc<208>();
     constexpr int COLS = C::COLS;
     // (warp and, below, row count from lane 0: the compiler then knows that the
     // lanes share them, and the loop runs 5 % faster)
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (GLU) t.b1 = __ldg(++t.w1);
         }
         const uint32_t b = it % C::NBUF;
-        ok = mbar_wait_warp<true>(smem_u32(acc_full + b), (it / C::NBUF) & 1, abort_flag, p.status, true,
+        ok = mbar_wait_warp(smem_u32(acc_full + b), (it / C::NBUF) & 1, abort_flag, p.status, true,
                             p.wait_limit);
         if (!ok) break;
         tc_fence_after();
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         am[half * BM + m] = mx;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(xchg));
-        ok = mbar_wait_warp<true>(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
+        ok = mbar_wait_warp(smem_u32(xchg), tiles & 1, abort_flag, p.status, true, p.wait_limit);
         if (!ok) break;
         if (m < nv) {
           mx = fmaxf(am[m], am[BM + m]);
