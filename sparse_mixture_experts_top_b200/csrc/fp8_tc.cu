@@ -37,12 +37,12 @@
 //     run to run.
 //
 // What bounds it, on one B200: many rows, the hand-over of the two accumulator
-// buffers and the clock under the power cap (4096 x 4096 x 7168: 119 us in a
-// burst, 137 us sustained, 0.61 and 0.53 of twice the measured bf16 rate; an
+// buffers and the clock under the power cap (4096 x 4096 x 7168: 117 us in a
+// burst, 133 us sustained, 0.62 and 0.55 of twice the measured bf16 rate; an
 // MMA with its commit, read-back and scaling, operands resident, takes 563 cycles
 // a k-block, the MMAs alone 512); few rows, the weights' bytes (down of 256 rows over 128 experts
 // 28 us, 0.97 of the measured HBM rate; gate|up of 20,480 rows over 512 experts
-// 216 us, 0.77). A pair of CTAs on one tile (cta_group::2) moves a third less
+// 206 us, 0.80). A pair of CTAs on one tile (cta_group::2) moves a third less
 // through shared memory but hands buffers over between SMs: 145 against 149 us
 // sustained, not kept; MMAs of N = 128 with four buffers read the token rows twice: slower.
 //
