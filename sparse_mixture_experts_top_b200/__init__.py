@@ -4,7 +4,9 @@ layer forward.
 Argument marshalling only: every function here checks shapes and dtypes,
 allocates outputs with PyTorch on the inputs' device, passes raw device
 pointers and the current CUDA stream to the C ABI (``include/moe.h``), and
-raises on a non-OK status. All arithmetic runs in the library's CUDA
+raises on a non-OK status. `stream=` makes a call as under
+``torch.cuda.stream(stream)``: its outputs belong to that stream, as those of
+torch's own operators would. All arithmetic runs in the library's CUDA
 kernels; there is no CPU path. Importing this module fails loudly if the
 library is missing or cannot be loaded.
 """
@@ -130,9 +132,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _under(stream, call, *args, **kw):
+    """`stream=` of a call: the call as made under torch.cuda.stream(stream), so
+    that the allocator hands out, and takes back, on that stream what the call
+    writes there. (A block of the current stream's pool may still be in use by
+    that stream's pending kernels, a call's scratch above all.)"""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
@@ -177,6 +187,8 @@ def experts_struct(ex) -> Experts:
 
 def route(x, w_router, router_bias, k, stream=None):
     """-> (logits fp32 [T,E], topk_idx int32 [T,k], topk_w fp32 [T,k])"""
+    if stream is not None:
+        return _under(stream, route, x, w_router, router_bias, k)
     _dev(x, w_router, router_bias)
     T, d = x.shape
     E = w_router.shape[0]
@@ -185,17 +197,19 @@ def route(x, w_router, router_bias, k, stream=None):
     idx = torch.empty(T, k, dtype=torch.int32, device=dev)
     w = torch.empty(T, k, dtype=torch.float32, device=dev)
     _check(lib.moe_route(_ptr(x), _dt(x), _ptr(w_router), _ptr(router_bias), T, d, E, k,
-                         _ptr(logits), _ptr(idx), _ptr(w), _stream(stream)), "moe_route")
+                         _ptr(logits), _ptr(idx), _ptr(w), _stream()), "moe_route")
     return logits, idx, w
 
 
 def topk(logits, k, stream=None):
     """-> (topk_idx int32 [T,k], topk_w fp32 [T,k]) from fp32 logits [T,E]"""
+    if stream is not None:
+        return _under(stream, topk, logits, k)
     _dev(logits)
     T, E = logits.shape
     idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
     w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
-    _check(lib.moe_topk(_ptr(logits), T, E, k, _ptr(idx), _ptr(w), _stream(stream)), "moe_topk")
+    _check(lib.moe_topk(_ptr(logits), T, E, k, _ptr(idx), _ptr(w), _stream()), "moe_topk")
     return idx, w
 
 
@@ -211,6 +225,8 @@ class SortTables:
 
 
 def sort_rows(topk_idx, E, BM, stream=None) -> SortTables:
+    if stream is not None:
+        return _under(stream, sort_rows, topk_idx, E, BM)
     _dev(topk_idx)
     T, k = topk_idx.shape
     R = T * k
@@ -223,12 +239,14 @@ def sort_rows(topk_idx, E, BM, stream=None) -> SortTables:
     ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
     _check(lib.moe_sort_rows(_ptr(topk_idx), T, k, E, BM, _ptr(order), _ptr(inv), _ptr(rmap),
                              _ptr(counts), _ptr(roff), _ptr(toff), _ptr(ws), nws,
-                             _stream(stream)), "moe_sort_rows")
+                             _stream()), "moe_sort_rows")
     return SortTables(order, inv, rmap, counts, roff, toff, BM)
 
 
 def grouped_swiglu(x, tables: SortTables, k, experts, regime=REGIME_AUTO, ws=None, stream=None):
     """-> h [T*k, F]: fp16 for bf16 or fp16 x, fp32 for fp32 x"""
+    if stream is not None:
+        return _under(stream, grouped_swiglu, x, tables, k, experts, regime, ws)
     _dev(x)
     T = x.shape[0]
     ex = experts_struct(experts)
@@ -239,7 +257,7 @@ def grouped_swiglu(x, tables: SortTables, k, experts, regime=REGIME_AUTO, ws=Non
         ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device)
     _check(lib.moe_grouped_swiglu(_ptr(x), _dt(x), _ptr(tables.row_map), _ptr(tables.row_off),
                                   _ptr(tables.tile_off), tables.BM, T, k, ctypes.byref(ex),
-                                  _ptr(h), _ptr(ws), ws.numel(), regime, _stream(stream)),
+                                  _ptr(h), _ptr(ws), ws.numel(), regime, _stream()),
            "moe_grouped_swiglu")
     return h
 
@@ -250,6 +268,8 @@ def grouped_down(h, tables: SortTables, T, k, experts, regime=REGIME_AUTO, strea
     `dtype` is the layer's activation type (torch.bfloat16, torch.float16 or
     torch.float32); it may be left out for fp32 h, which only fp32
     activations produce."""
+    if stream is not None:
+        return _under(stream, grouped_down, h, tables, T, k, experts, regime, dtype=dtype)
     _dev(h)
     ex = experts_struct(experts)
     if dtype is None:
@@ -264,12 +284,14 @@ def grouped_down(h, tables: SortTables, T, k, experts, regime=REGIME_AUTO, strea
     ys = torch.empty(T * k, experts.d, dtype=h.dtype, device=h.device)
     _check(lib.moe_grouped_down(_ptr(h), adt, _ptr(tables.row_off), _ptr(tables.tile_off),
                                 tables.BM, T, k, ctypes.byref(ex), _ptr(ys), regime,
-                                _stream(stream)), "moe_grouped_down")
+                                _stream()), "moe_grouped_down")
     return ys
 
 
 def combine(ys, inv_order, topk_w, T, k, dtype=torch.bfloat16, stream=None):
     """-> y [T, d] in `dtype` from ys [T*k, d] (fp16 for 16-bit `dtype`, fp32 for fp32)"""
+    if stream is not None:
+        return _under(stream, combine, ys, inv_order, topk_w, T, k, dtype)
     _dev(ys, inv_order, topk_w)
     want = torch.float32 if dtype == torch.float32 else torch.float16
     if ys.dtype != want:
@@ -277,8 +299,7 @@ def combine(ys, inv_order, topk_w, T, k, dtype=torch.bfloat16, stream=None):
     d = ys.shape[1]
     y = torch.empty(T, d, dtype=dtype, device=ys.device)
     _check(lib.moe_combine(_ptr(ys), _ptr(inv_order), _ptr(topk_w), T, k, d,
-                           _dt_of(dtype), _ptr(y),
-                           _stream(stream)), "moe_combine")
+                           _dt_of(dtype), _ptr(y), _stream()), "moe_combine")
     return y
 
 
@@ -335,6 +356,8 @@ def quantize_fp8(x, block=1, stream=None):
     elements (block=128: [ceil(rows/128), ceil(K/128)], for weights). A stack of
     weights x [E, rows, K] (rows a multiple of 128 for block=128) gives a stack
     of scales."""
+    if stream is not None:
+        return _under(stream, quantize_fp8, x, block)
     raw = _on(x)
     shape = x.shape
     if len(shape) < 2:
@@ -354,8 +377,7 @@ def quantize_fp8(x, block=1, stream=None):
             raise ValueError("a stack of weights needs rows in multiples of 128 (a block of "
                              "scales may not straddle two of them)")
         s = _empty(*shape[:-2], groups, -(-K // FP8_BLOCK), dtype=_F32, device=x.device)
-    st = lib.moe_quantize_fp8(x.data_ptr(), _dt(x), n, K, block, q.data_ptr(), s.data_ptr(),
-                              raw if stream is None else stream.cuda_stream)
+    st = lib.moe_quantize_fp8(x.data_ptr(), _dt(x), n, K, block, q.data_ptr(), s.data_ptr(), raw)
     if st:
         _check(st, "moe_quantize_fp8")
     return q, s
@@ -364,6 +386,8 @@ def quantize_fp8(x, block=1, stream=None):
 def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
     """y [M, N] = a . b^T in `dtype` from e4m3 codes a [M, K], b [N, K] and fp32
     scales sa [M, ceil(K/128)], sb [ceil(N/128), ceil(K/128)]."""
+    if stream is not None:
+        return _under(stream, fp8_matmul, a, sa, b, sb, dtype, out)
     raw = _on(a, sa, b, sb, out)
     _codes(a, 2, "a")
     _codes(b, 2, "b")
@@ -381,7 +405,7 @@ def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
     else:
         _is(out, dtype, (M, N), "out")
     st = lib.moe_fp8_matmul(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), M, N, K, dt,
-                            out.data_ptr(), raw if stream is None else stream.cuda_stream)
+                            out.data_ptr(), raw)
     if st:
         _check(st, "moe_fp8_matmul")
     return out
@@ -408,6 +432,8 @@ def _f8_experts(ex) -> Experts:
 def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUTO, stream=None):
     """-> (hq e4m3 [T*k, F], hs fp32 [T*k, F/128]): gate|up and GLU of f8 experts
     from quantised token rows xq [T, d], xs [T, d/128] (quantize_fp8)."""
+    if stream is not None:
+        return _under(stream, grouped_swiglu_fp8, xq, xs, tables, k, experts, regime)
     rmap, roff, toff = tables.row_map, tables.row_off, tables.tile_off
     raw = _on(xq, xs, rmap, roff, toff)
     _codes(xq, 2, "xq")
@@ -425,8 +451,7 @@ def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUT
     hs = _empty(R, -(-F // FP8_BLOCK), dtype=_F32, device=dev)
     st = lib.moe_grouped_swiglu_fp8(xq.data_ptr(), xs.data_ptr(), rmap.data_ptr(), roff.data_ptr(),
                                     toff.data_ptr(), tables.BM, T, k, ctypes.byref(ex),
-                                    hq.data_ptr(), hs.data_ptr(), regime,
-                                    raw if stream is None else stream.cuda_stream)
+                                    hq.data_ptr(), hs.data_ptr(), regime, raw)
     if st:
         _check(st, "moe_grouped_swiglu_fp8")
     return hq, hs
@@ -435,6 +460,8 @@ def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUT
 def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AUTO, stream=None):
     """-> ys fp16 [T*k, d] from quantised rows hq [T*k, F], hs [T*k, F/128]
     (grouped_swiglu_fp8)."""
+    if stream is not None:
+        return _under(stream, grouped_down_fp8, hq, hs, tables, T, k, experts, regime)
     roff, toff = tables.row_off, tables.tile_off
     raw = _on(hq, hs, roff, toff)
     _codes(hq, 2, "hq")
@@ -448,8 +475,7 @@ def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AU
     ex = _f8_experts(experts)
     ys = _empty(R, experts.d, dtype=torch.float16, device=hq.device)
     st = lib.moe_grouped_down_fp8(hq.data_ptr(), hs.data_ptr(), roff.data_ptr(), toff.data_ptr(),
-                                  tables.BM, T, k, ctypes.byref(ex), ys.data_ptr(), regime,
-                                  raw if stream is None else stream.cuda_stream)
+                                  tables.BM, T, k, ctypes.byref(ex), ys.data_ptr(), regime, raw)
     if st:
         _check(st, "moe_grouped_down_fp8")
     return ys
@@ -486,6 +512,8 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
     one where it is left out), from fp32 logits [T, E] and topk_idx int32 [T, k].
     mask [T]: tokens that are False take no part. ws: a uint8 tensor of
     moe_balance_loss_workspace bytes to reuse."""
+    if stream is not None:
+        return _under(stream, balance_loss, logits, topk_idx, coef, mask, seq_off, ws)
     raw = _on(logits, topk_idx, mask, seq_off, ws)
     T, E, B = _balance_sizes(logits, mask, seq_off)
     if topk_idx.dtype != _I32 or topk_idx.dim() != 2 or topk_idx.shape[0] != T:
@@ -501,12 +529,9 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
         need = lib.moe_balance_loss_workspace(T, E, B)
         if need:
             ws = _empty(need, dtype=_U8, device=dev)
-            if stream is not None:
-                ws.record_stream(stream)     # freed here, still in use there
     st = lib.moe_balance_loss(logits.data_ptr(), topk_idx.data_ptr(), _at(mask), _at(seq_off), T, E,
                               k, B, coef, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(),
-                              tokens.data_ptr(), _at(ws), 0 if ws is None else ws.nbytes,
-                              raw if stream is None else stream.cuda_stream)
+                              tokens.data_ptr(), _at(ws), 0 if ws is None else ws.nbytes, raw)
     if st:
         _check(st, "moe_balance_loss")
     return BalanceStats(loss, counts, probs, tokens)
@@ -516,6 +541,8 @@ def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_o
                           dloss=None, stream=None):
     """-> dlogits fp32 [T, E], the gradient of balance_loss(logits, ..., coef, mask,
     seq_off) times dloss (an fp32 tensor of one value; 1 where it is left out)."""
+    if stream is not None:
+        return _under(stream, balance_loss_backward, logits, stats, k, coef, mask, seq_off, dloss)
     counts, tokens = stats.counts, stats.tokens
     raw = _on(logits, counts, tokens, mask, seq_off, dloss)
     T, E, B = _balance_sizes(logits, mask, seq_off)
@@ -526,7 +553,7 @@ def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_o
     d = torch.empty_like(logits)
     st = lib.moe_balance_loss_backward(logits.data_ptr(), _at(mask), _at(seq_off), T, E, k, B, coef,
                                        counts.data_ptr(), tokens.data_ptr(), _at(dloss),
-                                       d.data_ptr(), raw if stream is None else stream.cuda_stream)
+                                       d.data_ptr(), raw)
     if st:
         _check(st, "moe_balance_loss_backward")
     return d
@@ -563,6 +590,8 @@ def forward_workspace(x, experts, k, regime=REGIME_AUTO):
 def forward(x, w_router, router_bias, experts, k, regime=REGIME_AUTO, ws=None, out=None,
             stream=None):
     """The whole layer: y [T, d] in x's dtype."""
+    if stream is not None:
+        return _under(stream, forward, x, w_router, router_bias, experts, k, regime, ws, out)
     _dev(x, w_router, router_bias)
     T = x.shape[0]
     ex = experts_struct(experts)
@@ -570,7 +599,7 @@ def forward(x, w_router, router_bias, experts, k, regime=REGIME_AUTO, ws=None, o
         ws = forward_workspace(x, experts, k, regime)
     y = out if out is not None else torch.empty(T, experts.d, dtype=x.dtype, device=x.device)
     _check(lib.moe_forward(_ptr(x), _dt(x), _ptr(w_router), _ptr(router_bias), ctypes.byref(ex),
-                           T, k, _ptr(y), _ptr(ws), ws.numel(), regime, _stream(stream)),
+                           T, k, _ptr(y), _ptr(ws), ws.numel(), regime, _stream()),
            "moe_forward")
     return y
 
@@ -579,6 +608,8 @@ def pack_gate_up(fmt, w_g, w_u, s_g=None, b_g=None, s_u=None, b_u=None, stream=N
     """Fused [gate|up] tensors (w_gu, s_gu, b_gu) from separate gate and up
     projections [E][F][...] on the device; s_gu, b_gu are None unless q4 or q8
     (f8 has s_gu alone)."""
+    if stream is not None:
+        return _under(stream, pack_gate_up, fmt, w_g, w_u, s_g, b_g, s_u, b_u)
     _dev(w_g, w_u, s_g, b_g, s_u, b_u)
     E, F = w_g.shape[0], w_g.shape[1]
     fmt_c = _FMT[fmt] if isinstance(fmt, str) else int(fmt)
@@ -595,7 +626,7 @@ def pack_gate_up(fmt, w_g, w_u, s_g=None, b_g=None, s_u=None, b_u=None, stream=N
                            device=s_g.device)
     _check(lib.moe_pack_gate_up(fmt_c, E, d, F, _ptr(w_g), _ptr(s_g), _ptr(b_g), _ptr(w_u),
                                 _ptr(s_u), _ptr(b_u), _ptr(w_gu), _ptr(s_gu), _ptr(b_gu),
-                                _stream(stream)), "moe_pack_gate_up")
+                                _stream()), "moe_pack_gate_up")
     return w_gu, s_gu, b_gu
 
 

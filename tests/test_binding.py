@@ -1,0 +1,155 @@
+"""What the Python binding does around a launch: where it allocates, what it
+refuses. CPU tests run the calls on meta tensors with the library faked; GPU
+tests run what only shows there."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+gpu = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import __graft_entry__
+    __graft_entry__.build()
+    import sparse_mixture_experts_top_b200 as m
+    return m
+
+
+class FakeLib:
+    """Every launch succeeds and is noted; a workspace takes 64 bytes."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            if name == "moe_forward_layout":
+                args[-1]._obj.total = 64
+            return 64 if name.endswith("workspace") else 0
+        return call
+
+
+def meta(*shape, dtype=torch.float32):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def f8_experts(E=8, d=256, F=128, **other):
+    u8 = torch.uint8
+    return types.SimpleNamespace(**{**dict(
+        fmt="f8", E=E, d=d, F=F, act="swiglu", w_gu=meta(E, 2 * F, d, dtype=u8),
+        s_gu=meta(E, 2 * F // 128, d // 128), b_gu=None, w_dn=meta(E, d, F, dtype=u8),
+        s_dn=meta(E, d // 128, F // 128), b_dn=None), **other})
+
+
+def sort_tables(moe, T, k, E, BM=128, **other):
+    i32, u32 = torch.int32, torch.uint32
+    return moe.SortTables(**{**dict(
+        order=meta(T * k, dtype=u32), inv_order=meta(T * k, dtype=u32),
+        row_map=meta(T * k, dtype=u32), counts=meta(E, dtype=i32),
+        row_off=meta(E + 1, dtype=i32), tile_off=meta(E + 1, dtype=i32), BM=BM), **other})
+
+
+@pytest.fixture
+def fake(moe, monkeypatch):
+    """The binding without a GPU: its device checks passed over, its launches
+    noted. `fake.inside`: a stream was entered by torch.cuda.stream."""
+    f = FakeLib()
+    f.inside = None
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, f.inside = f.inside, s
+        yield
+        f.inside = before
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(moe, "lib", f)
+    monkeypatch.setattr(moe, "_dev", lambda *ts: None)
+    monkeypatch.setattr(moe, "_on", lambda *ts: f.inside)
+    monkeypatch.setattr(moe, "_stream", lambda *s: f.inside)
+    return f
+
+
+# ------------------------------------------------------------------ stream=
+
+def calls(moe):
+    T, E, k, d, F = 4, 8, 2, 256, 128
+    bf, f16, i32, u8 = torch.bfloat16, torch.float16, torch.int32, torch.uint8
+    ex, st = f8_experts(), sort_tables(moe, T, k, E)
+    x, w, idx, lg = meta(T, d, dtype=bf), meta(E, d, dtype=bf), meta(T, k, dtype=i32), meta(T, E)
+    stats = moe.BalanceStats(meta(), meta(1, E, dtype=i32), meta(1, E), meta(1, dtype=i32))
+    return dict(
+        route=(x, w, None, k), topk=(lg, k), sort_rows=(idx, E, 128),
+        grouped_swiglu=(x, st, k, ex), grouped_down=(meta(T * k, F), st, T, k, ex),
+        combine=(meta(T * k, d, dtype=f16), st.inv_order, meta(T, k), T, k),
+        quantize_fp8=(x,), fp8_matmul=(meta(T, d, dtype=u8), meta(T, 2), meta(E, d, dtype=u8),
+                                       meta(1, 2)),
+        grouped_swiglu_fp8=(meta(T, d, dtype=u8), meta(T, 2), st, k, ex),
+        grouped_down_fp8=(meta(T * k, F, dtype=u8), meta(T * k, 1), st, T, k, ex),
+        balance_loss=(lg, idx, 1.0), balance_loss_backward=(lg, stats, k, 1.0),
+        forward=(x, w, None, ex, k),
+        pack_gate_up=("f8", meta(E, F, d, dtype=u8), meta(E, F, d, dtype=u8), meta(E, 1, 2), None,
+                      meta(E, 1, 2)))
+
+
+CALLS = ("route", "topk", "sort_rows", "grouped_swiglu", "grouped_down", "combine", "quantize_fp8",
+         "fp8_matmul", "grouped_swiglu_fp8", "grouped_down_fp8", "balance_loss",
+         "balance_loss_backward", "forward", "pack_gate_up")
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_on_another_stream_allocates_there(moe, fake, monkeypatch, name):
+    """A block from the current stream's pool may still be in use by that
+    stream's kernels when another stream's write it."""
+    args = calls(moe)[name]
+    made = []
+
+    def noting(make):
+        def f(*a, **kw):
+            made.append(fake.inside)
+            return make(*a, **kw)
+        return f
+
+    monkeypatch.setattr(torch, "empty", noting(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", noting(torch.empty_like))
+    monkeypatch.setattr(moe, "_empty", noting(moe._empty))
+    side = types.SimpleNamespace(cuda_stream=0x51DE)
+    getattr(moe, name)(*args, stream=side)
+    assert made and all(m is side for m in made)
+    launches = [a for n, a in fake.calls if n == "moe_" + name]
+    assert len(launches) == 1 and launches[0][-1] is side
+    assert fake.inside is None
+
+
+@gpu
+def test_balance_loss_beside_one_still_pending(moe):
+    """A call whose scratch has gone back to the current stream's pool while
+    its kernels still run, and one on another stream that starts at once."""
+    T, E, k = 200003, 64, 4
+    g = torch.Generator(device=DEV).manual_seed(0)
+    a, b = (torch.randn(T, E, generator=g, device=DEV) for _ in range(2))
+    ia, ib = (t.topk(k, 1).indices.int() for t in (a, b))
+    ra, rb = moe.balance_loss(a, ia, 1.0), moe.balance_loss(b, ib, 1.0)
+    qa, qb = moe.quantize_fp8(a), moe.quantize_fp8(b)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    for _ in range(5):
+        for _ in range(8):
+            busy.zero_()                       # the current stream falls behind
+        s = [moe.balance_loss(a, ia, 1.0) for _ in range(3)]
+        t = [moe.balance_loss(b, ib, 1.0, stream=side) for _ in range(3)]
+        q = moe.quantize_fp8(a)
+        r = moe.quantize_fp8(b, stream=side)
+        torch.cuda.synchronize()
+        for got, want in [(v, ra) for v in s] + [(v, rb) for v in t]:
+            assert torch.equal(got.loss, want.loss) and torch.equal(got.probs, want.probs)
+            assert torch.equal(got.counts, want.counts) and torch.equal(got.tokens, want.tokens)
+        for got, want in ((q, qa), (r, qb)):
+            assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
+            assert torch.equal(got[1], want[1])
