@@ -412,10 +412,12 @@ def fp8_matmul(a, sa, b, sb, dtype=torch.bfloat16, out=None, stream=None):
 
 
 def _f8_experts(ex) -> Experts:
-    """C view of f8 experts, whose shapes the grouped calls rely on."""
+    """C view of f8 experts, whose shapes and types the kernels rely on; experts
+    of another format as experts_struct has them (the fp8 stage calls of the
+    library refuse them)."""
     fmt = ex.fmt
     if fmt != "f8" and fmt != W_F8:
-        return experts_struct(ex)                    # the library refuses it
+        return experts_struct(ex)
     w_gu, s_gu, w_dn, s_dn, act = ex.w_gu, ex.s_gu, ex.w_dn, ex.s_dn, getattr(ex, "act", "swiglu")
     E, d, F, B = ex.E, ex.d, ex.F, FP8_BLOCK
     if w_gu.shape != (E, 2 * F, d) or w_dn.shape != (E, d, F):
@@ -594,7 +596,10 @@ def forward(x, w_router, router_bias, experts, k, regime=REGIME_AUTO, ws=None, o
         return _under(stream, forward, x, w_router, router_bias, experts, k, regime, ws, out)
     _dev(x, w_router, router_bias)
     T = x.shape[0]
-    ex = experts_struct(experts)
+    if x.shape != (T, experts.d) or w_router.shape != (experts.E, experts.d):
+        raise ValueError(f"x is {list(x.shape)} and w_router {list(w_router.shape)}, not "
+                         f"[T, {experts.d}] and [{experts.E}, {experts.d}]")
+    ex = _f8_experts(experts)
     if ws is None:
         ws = forward_workspace(x, experts, k, regime)
     y = out if out is not None else torch.empty(T, experts.d, dtype=x.dtype, device=x.device)

@@ -153,3 +153,45 @@ def test_balance_loss_beside_one_still_pending(moe):
         for got, want in ((q, qa), (r, qb)):
             assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
             assert torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------ refusals
+
+BAD_F8 = dict(
+    bf16_scales=lambda: dict(s_gu=meta(8, 2, 2, dtype=torch.bfloat16)),
+    bf16_down_scales=lambda: dict(s_dn=meta(8, 2, 1, dtype=torch.bfloat16)),
+    a_scale_per_row=lambda: dict(s_gu=meta(8, 256)),
+    gate_scales_alone=lambda: dict(s_gu=meta(8, 1, 2)),
+    no_expert_axis=lambda: dict(s_dn=meta(2, 1)),
+    codes_of_16_bits=lambda: dict(w_gu=meta(8, 256, 256, dtype=torch.bfloat16)),
+    gate_alone=lambda: dict(w_gu=meta(8, 128, 256, dtype=torch.uint8)),
+    down_transposed=lambda: dict(w_dn=meta(8, 128, 256, dtype=torch.uint8)),
+    fewer_experts=lambda: dict(w_dn=meta(7, 256, 128, dtype=torch.uint8)))
+
+
+@pytest.mark.parametrize("fmt", ["f8", 6])
+@pytest.mark.parametrize("name", ["forward", "grouped_swiglu_fp8", "grouped_down_fp8"])
+@pytest.mark.parametrize("bad", BAD_F8)
+def test_f8_experts_of_other_shapes_or_types_are_refused(moe, fake, name, bad, fmt):
+    """By the whole-layer call as by its stages: the kernels would read past
+    the end of such scales, or misread them."""
+    args = list(calls(moe)[name])
+    i = next(i for i, a in enumerate(args) if isinstance(a, types.SimpleNamespace))
+    args[i] = f8_experts(fmt=fmt)
+    getattr(moe, name)(*args)
+    assert len(fake.calls) >= 1
+    fake.calls.clear()
+    args[i] = f8_experts(fmt=fmt, **BAD_F8[bad]())
+    with pytest.raises((ValueError, TypeError)):
+        getattr(moe, name)(*args)
+    assert not fake.calls
+
+
+def test_rows_and_routers_of_another_width_are_refused(moe, fake):
+    x, w, _, ex, k = calls(moe)["forward"]
+    bf = torch.bfloat16
+    for bad in ((meta(4, 128, dtype=bf), w), (x, meta(8, 128, dtype=bf)), (x, meta(7, 256, dtype=bf)),
+                (meta(2, 2, 256, dtype=bf), w)):
+        with pytest.raises(ValueError):
+            moe.forward(*bad, None, ex, k)
+    assert not fake.calls
