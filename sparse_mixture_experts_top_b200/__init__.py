@@ -308,6 +308,7 @@ def combine(ys, inv_order, topk_w, T, k, dtype=torch.bfloat16, stream=None):
 F8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
+_ROWS = (torch.uint32, torch.int32)          # row numbers: below 2^31 either way
 _empty, _device, _raw_stream = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -431,6 +432,16 @@ def _f8_experts(ex) -> Experts:
                    s_dn.data_ptr(), None, _ACT[act] if isinstance(act, str) else int(act))
 
 
+def _tables_of(t: SortTables, R, E):
+    """sort_rows' tables of R rows and E experts: the kernels index by them."""
+    rows, roff, toff = t.row_map, t.row_off, t.tile_off
+    if rows.numel() != R or roff.numel() != E + 1 or toff.numel() != E + 1:
+        raise ValueError(f"the tables are of {rows.numel()} rows and {roff.numel() - 1} experts, "
+                         f"not {R} rows and {E}")
+    if roff.dtype != _I32 or toff.dtype != _I32:
+        raise ValueError(f"row_off and tile_off must be int32, got {roff.dtype} and {toff.dtype}")
+
+
 def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUTO, stream=None):
     """-> (hq e4m3 [T*k, F], hs fp32 [T*k, F/128]): gate|up and GLU of f8 experts
     from quantised token rows xq [T, d], xs [T, d/128] (quantize_fp8)."""
@@ -444,9 +455,9 @@ def grouped_swiglu_fp8(xq, xs, tables: SortTables, k, experts, regime=REGIME_AUT
         raise ValueError(f"xq is {list(xq.shape)}, the experts' d is {experts.d}")
     _is(xs, _F32, (T, -(-d // FP8_BLOCK)), "xs")
     R, F, E = T * k, experts.F, experts.E
-    if rmap.numel() != R or roff.numel() != E + 1 or toff.numel() != E + 1:
-        raise ValueError(f"the tables are of {rmap.numel()} rows and {roff.numel() - 1} experts, "
-                         f"not {T} x {k} rows and {E}")
+    _tables_of(tables, R, E)
+    if rmap.dtype not in _ROWS:
+        raise ValueError(f"row_map must be uint32 or int32, got {rmap.dtype}")
     ex = _f8_experts(experts)
     dev = xq.device
     hq = _empty(R, F, dtype=F8, device=dev)
@@ -471,9 +482,7 @@ def grouped_down_fp8(hq, hs, tables: SortTables, T, k, experts, regime=REGIME_AU
     if hq.shape != (R, F):
         raise ValueError(f"hq is {list(hq.shape)}, not [{T} x {k}, {F}]")
     _is(hs, _F32, (R, -(-F // FP8_BLOCK)), "hs")
-    if tables.row_map.numel() != R or roff.numel() != E + 1 or toff.numel() != E + 1:
-        raise ValueError(f"the tables are of {tables.row_map.numel()} rows and "
-                         f"{roff.numel() - 1} experts, not {T} x {k} rows and {E}")
+    _tables_of(tables, R, E)
     ex = _f8_experts(experts)
     ys = _empty(R, experts.d, dtype=torch.float16, device=hq.device)
     st = lib.moe_grouped_down_fp8(hq.data_ptr(), hs.data_ptr(), roff.data_ptr(), toff.data_ptr(),

@@ -195,3 +195,24 @@ def test_rows_and_routers_of_another_width_are_refused(moe, fake):
         with pytest.raises(ValueError):
             moe.forward(*bad, None, ex, k)
     assert not fake.calls
+
+
+@pytest.mark.parametrize("bad", [dict(row_off=torch.int64), dict(tile_off=torch.int64),
+                                 dict(row_off=torch.float32), dict(row_map=torch.int64),
+                                 dict(tile_off=torch.int16)])
+def test_tables_of_other_types_are_refused(moe, fake, bad):
+    """Tables of the right length whose entries have another width: the kernels
+    would read past their end, or rows that are not there."""
+    T, E, k = 4, 8, 2
+    n = dict(row_map=T * k, row_off=E + 1, tile_off=E + 1)
+    for name in ("grouped_swiglu_fp8", "grouped_down_fp8"):
+        if "row_map" in bad and name == "grouped_down_fp8":
+            continue                                   # takes the rows as they stand
+        args = list(calls(moe)[name])
+        args[2] = sort_tables(moe, T, k, E, **{f: meta(n[f], dtype=t) for f, t in bad.items()})
+        with pytest.raises(ValueError):
+            getattr(moe, name)(*args)
+    args = list(calls(moe)["grouped_swiglu_fp8"])
+    args[2] = sort_tables(moe, T, k, E, row_map=meta(T * k, dtype=torch.int32))
+    moe.grouped_swiglu_fp8(*args)
+    assert len(fake.calls) == 1
