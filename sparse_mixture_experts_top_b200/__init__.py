@@ -629,6 +629,9 @@ def pack_gate_up(fmt, w_g, w_u, s_g=None, b_g=None, s_u=None, b_u=None, stream=N
     fmt_c = _FMT[fmt] if isinstance(fmt, str) else int(fmt)
     per_word = {W_Q4G64: 8, W_Q4G32: 8, W_Q4G128: 8, W_Q8G64: 4}.get(fmt_c, 1)
     d = w_g.shape[2] * per_word
+    if w_u.shape != w_g.shape or w_u.element_size() != w_g.element_size():
+        raise ValueError(f"w_u must be {w_g.dtype} {list(w_g.shape)} as w_g is, got {w_u.dtype} "
+                         f"{list(w_u.shape)}")
     group = {W_Q4G64: 64, W_Q4G32: 32, W_Q4G128: 128, W_Q8G64: 64}.get(fmt_c, 0)
     w_gu = torch.empty((E, 2 * F) + tuple(w_g.shape[2:]), dtype=w_g.dtype, device=w_g.device)
     s_gu = b_gu = None
@@ -636,7 +639,13 @@ def pack_gate_up(fmt, w_g, w_u, s_g=None, b_g=None, s_u=None, b_u=None, stream=N
         s_gu = torch.empty((E, 2 * F, d // group), dtype=s_g.dtype, device=s_g.device)
         b_gu = torch.empty_like(s_gu)
     elif fmt_c == W_F8:
-        s_gu = torch.empty((E, 2 * s_g.shape[1], s_g.shape[2]), dtype=s_g.dtype,
+        _codes(w_g, 3, "w_g")
+        _codes(w_u, 3, "w_u")
+        for s, what in ((s_g, "s_g"), (s_u, "s_u")):
+            if s is None:
+                raise ValueError(f"f8 weights need {what}")
+            _is(s, _F32, (E, F // FP8_BLOCK, d // FP8_BLOCK), what)
+        s_gu = torch.empty((E, 2 * (F // FP8_BLOCK), d // FP8_BLOCK), dtype=_F32,
                            device=s_g.device)
     _check(lib.moe_pack_gate_up(fmt_c, E, d, F, _ptr(w_g), _ptr(s_g), _ptr(b_g), _ptr(w_u),
                                 _ptr(s_u), _ptr(b_u), _ptr(w_gu), _ptr(s_gu), _ptr(b_gu),

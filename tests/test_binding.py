@@ -216,3 +216,23 @@ def test_tables_of_other_types_are_refused(moe, fake, bad):
     args[2] = sort_tables(moe, T, k, E, row_map=meta(T * k, dtype=torch.int32))
     moe.grouped_swiglu_fp8(*args)
     assert len(fake.calls) == 1
+
+
+@pytest.mark.parametrize("bad", [
+    dict(w_u=(2, 128, 512)), dict(w_u=(2, 384, 256)), dict(w_u=(3, 256, 256)),
+    dict(s_u=(2, 1, 2)), dict(s_u=(2, 256)), dict(s_g=(2, 2, 1), s_u=(2, 2, 1)),
+    dict(s_g=(2, 256, 2), s_u=(2, 256, 2)), dict(s_g=torch.bfloat16, s_u=torch.bfloat16),
+    dict(s_u=torch.bfloat16), dict(w_g=torch.float16, w_u=torch.float16), dict(w_u=torch.bfloat16),
+    dict(s_g=None), dict(s_u=None)])
+def test_pack_gate_up_refuses_f8_parts_that_do_not_fit(moe, fake, bad):
+    good = dict(w_g=meta(2, 256, 256, dtype=torch.uint8), w_u=meta(2, 256, 256, dtype=torch.uint8),
+                s_g=meta(2, 2, 2), s_u=meta(2, 2, 2))
+    w, s, b = moe.pack_gate_up("f8", **good)
+    assert w.shape == (2, 512, 256) and s.shape == (2, 4, 2) and b is None
+    fake.calls.clear()
+    for n, v in bad.items():
+        good[n] = v if v is None else (good[n].to(v) if isinstance(v, torch.dtype)
+                                       else meta(*v, dtype=good[n].dtype))
+    with pytest.raises((ValueError, TypeError)):
+        moe.pack_gate_up("f8", **good)
+    assert not fake.calls
