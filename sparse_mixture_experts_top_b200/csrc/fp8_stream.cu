@@ -250,7 +250,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 3)
       float h = 0.f;
       float(*mx)[kTok] = s_max + (it & 1);
       if (threadIdx.x < kRows * kTok) {
-        h = glu(p.act, sum_warps<2, 1>(red, 0, row, tok), sum_warps<2, 1>(red, 1, row, tok));
+        h = glu_codes(p.act, sum_warps<2, 1>(red, 0, row, tok), sum_warps<2, 1>(red, 1, row, tok));
         float m = finite_abs(h);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -397,7 +397,7 @@ __device__ __forceinline__ void join_rows(const Params& p, const Unit& t, uint32
         float mx = 0.f, h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h[i] = glu(act_of(MODE), v[j][i], v[j][4 + i]);
+          h[i] = glu_codes(act_of(MODE), v[j][i], v[j][4 + i]);
           mx = fmaxf(mx, finite_abs(h[i]));
         }
 #pragma unroll
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
 #pragma unroll
           for (int j = 0; j < H; ++j) {
-            acc[j] = glu(act_of(MODE), acc[j], acc[H + j]);
+            acc[j] = glu_codes(act_of(MODE), acc[j], acc[H + j]);
             mx = fmaxf(mx, finite_abs(acc[j]));
           }
         }
