@@ -522,9 +522,15 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
     probabilities, per sequence (seq_off int32 [sequences + 1]; all tokens are
     one where it is left out), from fp32 logits [T, E] and topk_idx int32 [T, k].
     mask [T]: tokens that are False take no part. ws: a uint8 tensor of
-    moe_balance_loss_workspace bytes to reuse."""
+    moe_balance_loss_workspace bytes to reuse.
+
+    Logits that require a gradient give a loss that has one, by
+    balance_loss_backward. The counts are constants of it; a gradient that arrives
+    at probs, and a second derivative, are refused."""
     if stream is not None:
         return _under(stream, balance_loss, logits, topk_idx, coef, mask, seq_off, ws)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return BalanceStats(*_BalanceLoss.apply(logits, topk_idx, coef, mask, seq_off, ws))
     raw = _on(logits, topk_idx, mask, seq_off, ws)
     T, E, B = _balance_sizes(logits, mask, seq_off)
     if topk_idx.dtype != _I32 or topk_idx.dim() != 2 or topk_idx.shape[0] != T:
@@ -568,6 +574,33 @@ def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_o
     if st:
         _check(st, "moe_balance_loss_backward")
     return d
+
+
+class _BalanceLoss(torch.autograd.Function):
+    """balance_loss as a node of torch's graph (grad mode is off inside)."""
+
+    @staticmethod
+    def forward(ctx, logits, topk_idx, coef, mask, seq_off, ws):
+        s = balance_loss(logits, topk_idx, coef, mask, seq_off, ws)
+        ctx.k, ctx.coef = topk_idx.shape[1], coef
+        ctx.save_for_backward(logits, s.counts, s.tokens, mask, seq_off)
+        ctx.mark_non_differentiable(s.counts, s.tokens)
+        ctx.set_materialize_grads(False)
+        return s.loss, s.counts, s.probs, s.tokens
+
+    @staticmethod
+    def backward(ctx, dloss, dcounts, dprobs, dtokens):
+        if torch.is_grad_enabled():
+            raise RuntimeError("balance_loss is once differentiable (create_graph is not for it)")
+        if dprobs is not None:
+            raise RuntimeError("balance_loss: probs is a statistic without a gradient of its own "
+                               "(detach it)")
+        if dloss is None:
+            return (None,) * 6
+        logits, counts, tokens, mask, seq_off = ctx.saved_tensors
+        d = balance_loss_backward(logits, BalanceStats(None, counts, None, tokens), ctx.k, ctx.coef,
+                                  mask, seq_off, dloss)
+        return (d,) + (None,) * 5
 
 
 # ------------------------------------------------------------------ forward

@@ -236,3 +236,103 @@ def test_pack_gate_up_refuses_f8_parts_that_do_not_fit(moe, fake, bad):
     with pytest.raises((ValueError, TypeError)):
         moe.pack_gate_up("f8", **good)
     assert not fake.calls
+
+
+# ------------------------------------------------------------------ gradients
+
+def test_the_loss_is_a_node_of_the_graph_where_its_logits_are(moe, fake):
+    """No gradient is lost without a word (the launches are noted, not made)."""
+    lg, idx = meta(4, 8), meta(4, 2, dtype=torch.int32)
+    assert not moe.balance_loss(lg, idx, 1.0).loss.requires_grad
+    lg.requires_grad_()
+    with torch.no_grad():
+        assert not moe.balance_loss(lg, idx, 1.0).loss.requires_grad
+    fake.calls.clear()
+    s = moe.balance_loss(lg, idx, 1.0)
+    assert s.loss.requires_grad and not s.counts.requires_grad and not s.tokens.requires_grad
+    (d,) = torch.autograd.grad(s.loss * 2, lg)
+    assert d.shape == lg.shape
+    assert [n for n, _ in fake.calls if not n.endswith("workspace")] == \
+        ["moe_balance_loss", "moe_balance_loss_backward"]
+    fake.calls.clear()
+    s = moe.balance_loss(lg, idx, 1.0)
+    with pytest.raises(RuntimeError, match="probs"):
+        torch.autograd.grad((s.loss + s.probs.sum()), lg)
+    s = moe.balance_loss(lg, idx, 1.0)
+    with pytest.raises(RuntimeError, match="once differentiable"):
+        torch.autograd.grad(s.loss, lg, create_graph=True)
+    s = moe.balance_loss(lg, idx, 1.0)
+    s.counts.add_(1)                                    # what the gradient needs
+    with pytest.raises(RuntimeError, match="inplace"):
+        torch.autograd.grad(s.loss, lg)
+
+
+def _router_step(seed=0, T=3000, E=48, k=3, d=64):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(T, d, generator=g, device=DEV)
+    w = (torch.randn(E, d, generator=g, device=DEV) / 8).requires_grad_()
+    mask = torch.rand(T, generator=g, device=DEV) < 0.8
+    off = torch.tensor([10, 900, 900, T - 7], dtype=torch.int32, device=DEV)
+    idx = (x @ w.detach().t()).topk(k, 1).indices.int()
+    return x, w, idx, mask, off, k
+
+
+@gpu
+@pytest.mark.parametrize("T", [100, 3000])
+def test_a_router_trains_through_the_loss(moe, T):
+    """The gradient of the router's weight is that of balance_loss_backward, bit
+    for bit, beside another loss and on another stream."""
+    x, w, idx, mask, off, k = _router_step(T=T)
+    off = off if T > 1000 else None
+    with torch.no_grad():
+        lg = x @ w.t()
+        s = moe.balance_loss(lg, idx, 0.7, mask, off)
+        d = moe.balance_loss_backward(lg, s, k, 0.7, mask, off,
+                                      dloss=torch.tensor(3.0, device=DEV))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        lg = x @ w.t()
+        side.wait_stream(torch.cuda.current_stream())
+        t = moe.balance_loss(lg, idx, 0.7, mask, off, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(t.loss.detach(), s.loss) and torch.equal(t.counts, s.counts)
+        (got,) = torch.autograd.grad(3 * t.loss, lg)
+        assert torch.equal(got, d)
+    lg = x @ w.t()
+    t = moe.balance_loss(lg, idx, 0.7, mask, off)
+    (both,) = torch.autograd.grad(3 * t.loss + (lg * lg).mean(), w)
+    lg2 = x @ w.t()
+    (other,) = torch.autograd.grad((lg2 * lg2).mean(), w)
+    want = d.double().t() @ x.double() + other.double()
+    # fp32 products of T addends
+    size = d.abs().double().t() @ x.abs().double() + other.abs().double() + \
+        (2 / lg.numel() * lg.abs()).double().t() @ x.abs().double()
+    assert ((both.double() - want).abs() <= (T + 8) * 2.0 ** -23 * size).all()
+
+
+@gpu
+def test_a_training_step_in_a_graph(moe):
+    """Forward and backward captured together, replayed on new logits."""
+    x, w, idx, mask, off, k = _router_step(1)
+
+    def step():
+        lg = x @ w.t()
+        s = moe.balance_loss(lg, idx, 0.7, mask, off)
+        return s.loss.detach(), torch.autograd.grad(s.loss, w)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss, grad = step()
+    for seed in (2, 3):
+        x.copy_(_router_step(seed)[0])
+        g.replay()
+        torch.cuda.synchronize()
+        l2, g2 = step()
+        assert torch.equal(loss, l2) and torch.equal(grad, g2)
