@@ -54,7 +54,7 @@
  *     activations, quantised (q4 / q8) weights take bf16 or fp16 ones. Violations return MOE_ERR_INVALID_ARG or
  *     MOE_ERR_UNSUPPORTED.
  *   - All layouts are row-major with the stated shapes; buffers must be
- *     16-byte aligned.
+ *     16-byte aligned, except where a call says 4 bytes.
  *   - Calls are reentrant and keep no state between calls, apart from the
  *     device status word above, the no-allocation sort's scratch array
  *     (moe_sort_rows_noalloc) and the wait bound (moe_set_wait_cycles).
@@ -319,7 +319,7 @@ moe_status moe_forward(const void* x, moe_dtype dt, const void* w_router, const 
  *         s [ceil(rows/128)][ceil(K/128)] (weights; a stack of matrices whose
  *         row counts are multiples of 128 may be given as one)
  *   q     (device, out) e4m3 [rows][K]
- *   s     (device, out) fp32
+ *   s     (device, out) fp32, 4-byte aligned
  * rows and K are at most 2^30. The last block of a row (or of the rows) may be
  * partial. rows = 0 returns MOE_OK and launches nothing. */
 moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int block, void* q,
@@ -330,6 +330,7 @@ moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int bl
  *   y[m][n] = sum_kb sa[m][kb] sb[n/128][kb] sum_{k in block kb} a[m][k] b[n][k]
  *   a  (device) e4m3 [M][K], sa fp32 [M][ceil(K/128)]
  *   b  (device) e4m3 [N][K], sb fp32 [ceil(N/128)][ceil(K/128)]
+ *   sa and sb are 4-byte aligned: rows of a tensor, or one expert of a stack
  *   y  (device, out) [M][N], dtype dt; fp32 sums, rounded once. MOE_F16: values
  *      outside the fp16 range are reported as MOE_ERR_RANGE in the device
  *      status
@@ -341,7 +342,8 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
 /* moe_grouped_swiglu for MOE_W_F8 experts: gate|up of the sorted rows, the GLU,
  * and its result quantised in the same launch.
  *   xq, xs   (device) e4m3 token rows [T][d] and scales [T][d/128], in token
- *            order (moe_quantize_fp8, block 1); read in place through row_map
+ *            order (moe_quantize_fp8, block 1); read in place through row_map.
+ *            xs and hs are 4-byte aligned
  *   row_map, row_off, tile_off, BM: as for moe_grouped_swiglu
  *   hq, hs   (device, out) e4m3 [T*k][F] and fp32 [T*k][F/128]:
  *            h = act(g) * u in fp32, quantised as moe_quantize_fp8 (block 1)
@@ -356,7 +358,7 @@ moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_
                                   moe_regime regime, moe_stream_t stream);
 
 /* moe_grouped_down for MOE_W_F8 experts.
- *   hq, hs   (device) as moe_grouped_swiglu_fp8 writes them
+ *   hq, hs   (device) as moe_grouped_swiglu_fp8 writes them; hs 4-byte aligned
  *   ys       (device, out) [T*k][d] fp16, as moe_grouped_down stores it for
  *            16-bit activations (moe_combine reads it; values outside the fp16
  *            range are reported as MOE_ERR_RANGE in the device status) */
@@ -375,7 +377,8 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
  *   loss = coef/n_seq sum_b E/(k n_b) sum_e counts[b][e] probs[b][e]
  * so a uniform router has loss = coef. A sequence without valid tokens has
  * zeros and adds nothing (it still counts in n_seq).
- *   logits   (device) fp32 [T][E], as moe_route writes them
+ *   logits   (device) fp32 [T][E], as moe_route writes them; 4-byte aligned
+ *            where E is not a multiple of 4
  *   topk_idx (device) int32 [T][k]; ids outside [0, E) are not counted (slots
  *            that were dropped)
  *   mask     (device) uint8 [T], 0: the token takes no part and its logits are
@@ -409,7 +412,7 @@ moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const 
  *   logits, mask, seq_off, T, E, k, n_seq, coef: as given to moe_balance_loss
  *   counts, tokens (device): as it wrote them
  *   dloss    (device) fp32 [1]: the loss's own gradient; NULL: 1
- *   dlogits  (device, out) fp32 [T][E]
+ *   dlogits  (device, out) fp32 [T][E], aligned as logits
  * T = 0 returns MOE_OK and launches nothing. */
 moe_status moe_balance_loss_backward(const float* logits, const uint8_t* mask,
                                      const int32_t* seq_off, int T, int E, int k, int n_seq,

@@ -34,6 +34,9 @@ long long wait_cycles() {
 }
 
 static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// fp32 values that kernels take one by one (scales, rows of logits that no
+// vector covers): any view of a tensor
+static inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 static inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 static inline size_t act_size(int dt) { return dt == MOE_F32 ? 4 : 2; }
 
@@ -384,7 +387,7 @@ moe_status moe_quantize_fp8(const void* x, moe_dtype dt, int rows, int K, int bl
   if (K % 16 || rows > kMaxSize || K > kMaxSize) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !q || !s) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(s)) return MOE_ERR_INVALID_ARG;
   return launched(launch_quantize_fp8(x, dt, rows, K, block, q, s, (cudaStream_t)stream));
 }
 
@@ -395,7 +398,7 @@ moe_status moe_fp8_matmul(const void* a, const float* sa, const void* b, const f
   if (K % 16 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!a || !sa || !b || !sb || !y) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
+  if (!aligned16(a) || !aligned4(sa) || !aligned16(b) || !aligned4(sb) || !aligned16(y))
     return MOE_ERR_INVALID_ARG;
   // Up to 8 rows the weight-streaming kernel is the faster one until the weights
   // are large (one row, on one B200: N = 256, K = 2048 2.9 against 4.6 us,
@@ -421,7 +424,7 @@ moe_status moe_grouped_swiglu_fp8(const void* xq, const float* xs, const uint32_
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (!xq || !xs || !row_map || !row_off || !tile_off || !hq || !hs) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(xq) || !aligned16(xs) || !aligned16(hq) || !aligned16(hs))
+  if (!aligned16(xq) || !aligned4(xs) || !aligned16(hq) || !aligned4(hs))
     return MOE_ERR_INVALID_ARG;
   int rg = resolve_fp8(regime, (long long)T * k, experts->E, experts->F);
   if (regime == MOE_REGIME_AUTO && BM != tc_block_m()) rg = MOE_REGIME_GEMV;
@@ -438,7 +441,7 @@ moe_status moe_grouped_down_fp8(const void* hq, const float* hs, const int32_t* 
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (!hq || !hs || !row_off || !tile_off || !ys) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(hq) || !aligned16(hs) || !aligned16(ys)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(hq) || !aligned4(hs) || !aligned16(ys)) return MOE_ERR_INVALID_ARG;
   int rg = resolve_fp8(regime, (long long)T * k, experts->E, experts->d);
   if (regime == MOE_REGIME_AUTO && BM != tc_block_m()) rg = MOE_REGIME_GEMV;
   if (rg == MOE_REGIME_TC && BM != tc_block_m()) return MOE_ERR_INVALID_ARG;
@@ -461,6 +464,9 @@ static moe_status check_balance(const int32_t* seq_off, int T, int E, int k, int
   return n_seq > kMaxSeqs || T > kMaxSize ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// rows of E logits, read four at a time where E is a multiple of four
+static bool aligned_rows(const float* p, int E) { return E % 4 ? aligned4(p) : aligned16(p); }
+
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                             const int32_t* seq_off, int T, int E, int k, int n_seq, float coef,
                             float* loss, int32_t* counts, float* probs, int32_t* tokens, void* ws,
@@ -469,7 +475,7 @@ moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const 
   if (st != MOE_OK) return st;
   if (!loss || !counts || !probs || !tokens) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(logits)) return MOE_ERR_INVALID_ARG;
+  if (!aligned_rows(logits, E)) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_balance_loss_workspace(T, E, n_seq);
   if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   return launched(launch_balance_loss(logits, topk_idx, mask, seq_off, T, E, k, n_seq, coef, loss,
@@ -484,7 +490,7 @@ moe_status moe_balance_loss_backward(const float* logits, const uint8_t* mask,
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (!logits || !counts || !tokens || !dlogits) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(logits) || !aligned16(dlogits)) return MOE_ERR_INVALID_ARG;
+  if (!aligned_rows(logits, E) || !aligned_rows(dlogits, E)) return MOE_ERR_INVALID_ARG;
   return launched(launch_balance_loss_backward(logits, mask, seq_off, T, E, k, n_seq, coef, counts,
                                                tokens, dloss, dlogits, (cudaStream_t)stream));
 }

@@ -2,10 +2,13 @@
 refuses. CPU tests run the calls on meta tensors with the library faked; GPU
 tests run what only shows there."""
 import contextlib
+import ctypes
 import types
 
 import pytest
 import torch
+
+import moe_inputs as mi
 
 gpu = pytest.mark.gpu
 DEV = "cuda"
@@ -336,3 +339,91 @@ def test_a_training_step_in_a_graph(moe):
         torch.cuda.synchronize()
         l2, g2 = step()
         assert torch.equal(loss, l2) and torch.equal(grad, g2)
+
+
+# ------------------------------------------------------------------ alignment
+
+def test_scales_off_a_float_boundary_are_refused(moe):
+    L, P, ARG = moe.lib, None, moe.ERR_INVALID_ARG
+    p, off = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10002)
+    assert L.moe_quantize_fp8(p, moe.BF16, 4, 128, 1, p, off, P) == ARG
+    for i in (1, 3):
+        a = [p, p, p, p]
+        a[i] = off
+        assert L.moe_fp8_matmul(*a, 4, 8, 128, moe.BF16, p, P) == ARG
+    e = ctypes.byref(moe.Experts(moe.W_F8, 8, 256, 128, 0x10000, 0x10000, None, 0x10000, 0x10000,
+                                 None))
+    assert L.moe_grouped_swiglu_fp8(p, off, p, p, p, 128, 4, 2, e, p, p, 0, P) == ARG
+    assert L.moe_grouped_swiglu_fp8(p, p, p, p, p, 128, 4, 2, e, p, off, 0, P) == ARG
+    assert L.moe_grouped_down_fp8(p, off, p, p, 128, 4, 2, e, p, 0, P) == ARG
+    for lg, E in ((off, 33), (ctypes.c_void_p(0x10004), 32)):
+        assert L.moe_balance_loss(lg, p, P, P, 4, E, 2, 1, 1.0, p, p, p, p, p, 1 << 20, P) == ARG
+        assert L.moe_balance_loss_backward(lg, P, P, 4, E, 2, 1, 1.0, p, p, P, p, P) == ARG
+        assert L.moe_balance_loss_backward(p, P, P, 4, E, 2, 1, 1.0, p, p, P, lg, P) == ARG
+
+
+def _floats(t):
+    """A copy of fp32 t that starts 4 bytes into an allocation."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    return buf[1:].view(t.shape).copy_(t)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(5, 256, 384), (40, 640, 2064), (1000, 2100, 768)])
+def test_products_of_views(moe, M, N, K):
+    """Rows of a batch, one expert of a stack: views whose scales start at any
+    float give the bits of copies."""
+    g = torch.Generator(device=DEV).manual_seed(M)
+    a, sa = moe.quantize_fp8(torch.randn(M + 1, K, generator=g, device=DEV))
+    Nb = -(-N // 128) * 128
+    b, sb = moe.quantize_fp8(torch.randn(3, Nb, K, generator=g, device=DEV), 128)
+    want = moe.fp8_matmul(a[1:].clone(), sa[1:].clone(), b[1, :N].clone(), sb[1].clone())
+    assert torch.equal(moe.fp8_matmul(a[1:], sa[1:], b[1, :N], sb[1]), want)
+    want = moe.fp8_matmul(a, sa, b[1, :N], sb[1].clone())
+    assert torch.equal(moe.fp8_matmul(a, _floats(sa), b[1, :N], _floats(sb[1])), want)
+
+
+@gpu
+@pytest.mark.parametrize("regime", [1, 2])
+def test_expert_stages_of_views(moe, regime):
+    T, E, k, d, F = 70, 8, 2, 384, 128
+    ex = mi.make_experts(mi.Workload("f8", 1, d, E, 1, F, "bf16", "f8"), 3, DEV)
+    idx = mi.random_topk_idx(T, E, k, 1).to(DEV)
+    st = moe.sort_rows(idx, E, 128)
+    xq, xs = moe.quantize_fp8(torch.randn(T + 1, d, device=DEV))
+    want = moe.grouped_swiglu_fp8(xq[1:].clone(), xs[1:].clone(), st, k, ex, regime)
+    hq, hs = moe.grouped_swiglu_fp8(xq[1:], xs[1:], st, k, ex, regime)
+    assert torch.equal(hq.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(hs, want[1])
+    ys = moe.grouped_down_fp8(hq, hs, st, T, k, ex, regime)
+    assert torch.equal(moe.grouped_down_fp8(hq, _floats(hs), st, T, k, ex, regime), ys)
+    # scales written at such a place through the C calls
+    s = torch.cuda.current_stream().cuda_stream
+    e = moe.experts_struct(ex)
+    buf = torch.full((hs.numel() + 2,), -1.0, device=DEV)
+    h2 = torch.empty_like(hq)
+    assert moe.lib.moe_grouped_swiglu_fp8(
+        xq[1:].data_ptr(), xs[1:].data_ptr(), st.row_map.data_ptr(), st.row_off.data_ptr(),
+        st.tile_off.data_ptr(), 128, T, k, ctypes.byref(e), h2.data_ptr(), buf[1:].data_ptr(),
+        regime, s) == moe.OK
+    assert torch.equal(buf[1:-1].view_as(hs), hs) and buf[0] == -1 and buf[-1] == -1
+    x = torch.randn(9, 384, device=DEV)
+    q, sq = moe.quantize_fp8(x)
+    buf = torch.full((sq.numel() + 2,), -1.0, device=DEV)
+    assert moe.lib.moe_quantize_fp8(x.data_ptr(), moe.F32, 9, 384, 1, q.data_ptr(),
+                                    buf[1:].data_ptr(), s) == moe.OK
+    assert torch.equal(buf[1:-1].view_as(sq), sq) and buf[0] == -1 and buf[-1] == -1
+
+
+@gpu
+@pytest.mark.parametrize("T,E", [(40, 33), (9000, 65), (700, 510)])
+def test_balance_loss_of_a_batch_s_rows(moe, T, E):
+    """Logits from any row of a batch whose rows are no multiple of 16 bytes."""
+    g = torch.Generator(device=DEV).manual_seed(E)
+    lg = torch.randn(T + 1, E, generator=g, device=DEV)
+    idx = lg.topk(3, 1).indices.int()
+    want = moe.balance_loss(lg[1:].clone(), idx[1:].clone(), 1.0)
+    got = moe.balance_loss(lg[1:], idx[1:], 1.0)
+    assert torch.equal(got.loss, want.loss) and torch.equal(got.probs, want.probs)
+    assert torch.equal(got.counts, want.counts)
+    d = moe.balance_loss_backward(lg[1:], got, 3, 1.0)
+    assert torch.equal(d, moe.balance_loss_backward(lg[1:].clone(), want, 3, 1.0))
