@@ -344,7 +344,7 @@ def _codes(t, dims, what):
 def _sizes(*ns):
     """The library's size limit, which a larger Python int would slip past as a C int."""
     if max(ns) > 1 << 30:
-        raise ValueError(f"sizes {list(ns)}: rows, columns and tokens are limited to 2^30 each")
+        raise ValueError(f"sizes {list(ns)} are limited to 2^30 each")
 
 
 def _at(t):
@@ -506,13 +506,14 @@ def _balance_sizes(logits, mask, seq_off):
     if logits.dtype != _F32 or logits.dim() != 2:
         raise ValueError(f"logits must be fp32 [T, E], got {logits.dtype} {list(logits.shape)}")
     T, E = logits.shape
-    _sizes(T)
+    _sizes(T, E)
     if mask is not None and (mask.dtype not in (torch.bool, _U8) or mask.shape != (T,)):
         raise ValueError(f"mask must be bool or uint8 [{T}], got {mask.dtype} {list(mask.shape)}")
     if seq_off is None:
         return T, E, 1
     if seq_off.dtype != _I32 or seq_off.dim() != 1 or seq_off.numel() < 2:
         raise ValueError("seq_off must be int32 [sequences + 1]")
+    _sizes(seq_off.numel())
     return T, E, seq_off.numel() - 1
 
 
@@ -537,6 +538,7 @@ def balance_loss(logits, topk_idx, coef, mask=None, seq_off=None, ws=None,
         raise ValueError(f"topk_idx must be int32 [{T}, k], got {topk_idx.dtype} "
                          f"{list(topk_idx.shape)}")
     k = topk_idx.shape[1]
+    _sizes(k)
     dev = logits.device
     loss = torch.empty((), dtype=_F32, device=dev)
     probs = _empty(B, E, dtype=_F32, device=dev)
@@ -563,6 +565,7 @@ def balance_loss_backward(logits, stats: BalanceStats, k, coef, mask=None, seq_o
     counts, tokens = stats.counts, stats.tokens
     raw = _on(logits, counts, tokens, mask, seq_off, dloss)
     T, E, B = _balance_sizes(logits, mask, seq_off)
+    _sizes(k)
     _is(counts, _I32, (B, E), "stats.counts")
     _is(tokens, _I32, (B,), "stats.tokens")
     if dloss is not None and (dloss.dtype != _F32 or dloss.numel() != 1):

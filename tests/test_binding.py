@@ -241,6 +241,26 @@ def test_pack_gate_up_refuses_f8_parts_that_do_not_fit(moe, fake, bad):
     assert not fake.calls
 
 
+@pytest.mark.parametrize("n", [(1 << 30) + 1, (1 << 32) + 8])
+def test_balance_sizes_past_a_c_int_are_refused(moe, fake, n):
+    """Not cut to their low bits: experts, slots and sequences as tokens are."""
+    i32 = torch.int32
+    lg, idx = meta(4, 8), meta(4, 2, dtype=i32)
+    stats = moe.BalanceStats(meta(), meta(1, 8, dtype=i32), meta(1, 8), meta(1, dtype=i32))
+    wide = moe.BalanceStats(meta(), meta(1, n, dtype=i32), meta(1, n), meta(1, dtype=i32))
+    many = moe.BalanceStats(meta(), meta(n - 1, 8, dtype=i32), meta(n - 1, 8), meta(n - 1, dtype=i32))
+    off = meta(n, dtype=i32)
+    for call in (lambda: moe.balance_loss(meta(0, n), meta(0, 2, dtype=i32), 1.0),
+                 lambda: moe.balance_loss(meta(0, 8), meta(0, n, dtype=i32), 1.0),
+                 lambda: moe.balance_loss(lg, idx, 1.0, seq_off=off),
+                 lambda: moe.balance_loss_backward(lg, stats, n, 1.0),
+                 lambda: moe.balance_loss_backward(meta(0, n), wide, 2, 1.0),
+                 lambda: moe.balance_loss_backward(lg, many, 2, 1.0, seq_off=off)):
+        with pytest.raises(ValueError, match="2\\^30"):
+            call()
+    assert not fake.calls
+
+
 # ------------------------------------------------------------------ gradients
 
 def test_the_loss_is_a_node_of_the_graph_where_its_logits_are(moe, fake):
