@@ -309,7 +309,12 @@ F8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
 _ROWS = (torch.uint32, torch.int32)          # row numbers: below 2^31 either way
-_empty, _device, _raw_stream = torch.empty, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
+# the current device and its current stream's handle, by torch's own shortcuts
+# where it has them (the public calls take about a microsecond more)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _on(*ts):

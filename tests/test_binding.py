@@ -3,6 +3,9 @@ refuses. CPU tests run the calls on meta tensors with the library faked; GPU
 tests run what only shows there."""
 import contextlib
 import ctypes
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -447,3 +450,41 @@ def test_balance_loss_of_a_batch_s_rows(moe, T, E):
     assert torch.equal(got.counts, want.counts)
     d = moe.balance_loss_backward(lg[1:], got, 3, 1.0)
     assert torch.equal(d, moe.balance_loss_backward(lg[1:].clone(), want, 3, 1.0))
+
+
+# ------------------------------------------------------------------ torch
+
+NO_SHORTCUTS = """
+import torch
+had = {n: getattr(torch._C, n) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream")
+       if hasattr(torch._C, n)}
+for n in had:
+    delattr(torch._C, n)
+import sparse_mixture_experts_top_b200 as moe
+for n in had:                  # (torch's public calls may use them themselves)
+    setattr(torch._C, n, had[n])
+"""
+
+
+def _without_shortcuts(code):
+    r = subprocess.run([sys.executable, "-c", NO_SHORTCUTS + code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
+
+
+def test_the_binding_needs_no_private_name_of_torch(moe):
+    _without_shortcuts("assert callable(moe._device) and callable(moe._raw_stream)")
+
+
+@gpu
+def test_calls_without_private_names_of_torch(moe):
+    _without_shortcuts("""
+x = torch.randn(4, 256, device="cuda")
+q, s = moe.quantize_fp8(x)
+assert moe._raw_stream(0) == torch.cuda.current_stream().cuda_stream and moe._device() == 0
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+q2, s2 = moe.quantize_fp8(x, stream=side)
+torch.cuda.synchronize()
+assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+""")
