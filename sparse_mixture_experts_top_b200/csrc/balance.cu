@@ -10,7 +10,8 @@
 //
 // LPR lanes take a token (fewer than a warp where the row has fewer than 128
 // experts): its row stays in registers between the maximum, the sum and their
-// use, so each pass reads the logits once, and HBM bounds both. A lane group
+// use, so each pass reads the logits once. HBM bounds the backward pass, latency
+// (the ends of chunks, the second kernel) the forward one. A lane group
 // loads the rows of up to four tokens before it looks at the first, since a
 // single row's chain (load, maximum, exponentials, sum) is all latency.
 // The forward pass adds a CTA's tokens in registers and shared memory, writes

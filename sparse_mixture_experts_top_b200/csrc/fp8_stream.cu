@@ -17,8 +17,8 @@
 // conversion, nothing staged.
 //
 // Bound by latency at these sizes (one B200: one row, N = 4096, K = 7168, 29 MB of
-// codes, 8 us, 0.56 of the measured HBM rate; one token through 8 of 128 experts'
-// gate|up, 25 MB, 10.3 us): every warp has up to four k-blocks of weights on
+// codes, 8.9 us, 0.50 of the measured HBM rate; one token through 8 of 128 experts'
+// gate|up, 25 MB, 10.0 us, 0.38): every warp has up to four k-blocks of weights on
 // their way, three CTAs (gate|up) or two share an SM.
 //
 // gate|up: eight such CTAs form a cluster that covers 128 features, the block

@@ -20,8 +20,9 @@
 // scale, add and store: warp w reads TMEM lanes 32 (w % 4) .., and half (w - 4) / 4 of the
 // columns. Register shares: 88 per thread for warps 0..3, 208 for warps 4..11
 // (their sums of up to 128 columns live in registers), 168 at launch: 128 x 88 +
-// 256 x 208 = 384 x 168. With 72 and 216 the gathering warps spilled (gate|up of
-// 20,480 rows over 512 experts 264 against 246 us sustained).
+// 256 x 208 = 384 x 168. With 72 and 216 the gathering warps spilled more (gate|up of
+// 20,480 rows over 512 experts 257 against 238 us sustained); with these the gate|up
+// forms spill 24 or 36 bytes a thread and the 16-bit persistent ones 20.
 //
 // gate|up: the unit's weight rows are 128 gate and the 128 up rows of the same
 // features, so a thread holds both for 64 features; the GLU's result is
@@ -37,14 +38,16 @@
 //     run to run.
 //
 // What bounds it, on one B200: many rows, the hand-over of the two accumulator
-// buffers and the clock under the power cap (4096 x 4096 x 7168: 117 us in a
-// burst, 133 us sustained, 0.62 and 0.55 of twice the measured bf16 rate; an
-// MMA with its commit, read-back and scaling, operands resident, takes 563 cycles
-// a k-block, the MMAs alone 512); few rows, the weights' bytes (down of 256 rows over 128 experts
-// 28 us, 0.97 of the measured HBM rate; gate|up of 20,480 rows over 512 experts
-// 206 us, 0.80). A pair of CTAs on one tile (cta_group::2) moves a third less
-// through shared memory but hands buffers over between SMs: 145 against 149 us
-// sustained, not kept; MMAs of N = 128 with four buffers read the token rows twice: slower.
+// buffers and the clock under the power cap (4096 x 4096 x 7168: 116 us in a
+// burst, 134 us sustained, 0.63 and 0.54 of twice the measured bf16 rate: 902 cycles
+// a k-block; an MMA with its commit, read-back and scaling, operands resident, takes
+// 563, the MMAs alone 512, and the 48 KB that a k-block writes to and the 48 KB that
+// it reads from shared memory 768 at 128 bytes a cycle); few rows, the weights' bytes
+// (down of 256 rows over 128 experts 27.4 us, 0.99 of the measured HBM rate; gate|up of
+// 20,480 rows over 512 experts 204 us, 0.81). A pair of CTAs on one tile (cta_group::2) moves a
+// third less through shared memory but hands buffers over between SMs: 145 against
+// 149 us sustained in an earlier state of the kernel, not kept and not measured
+// again since; MMAs of N = 128 with four buffers read the token rows twice: slower.
 //
 // Every mbarrier wait is bounded, as in the other tensor-core kernels; the
 // cluster barriers are reached by every thread, whatever the waits did.
