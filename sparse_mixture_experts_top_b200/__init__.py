@@ -5,8 +5,8 @@ Argument marshalling only: every function here checks shapes and dtypes,
 allocates outputs with PyTorch on the inputs' device, passes raw device
 pointers and the current CUDA stream to the C ABI (``include/moe.h``), and
 raises on a non-OK status. `stream=` makes a call as under
-``torch.cuda.stream(stream)``: its outputs belong to that stream, as those of
-torch's own operators would. All arithmetic runs in the library's CUDA
+``torch.cuda.stream(stream)``; the caller orders its own reads after that
+stream's work. All arithmetic runs in the library's CUDA
 kernels; there is no CPU path. Importing this module fails loudly if the
 library is missing or cannot be loaded.
 """
@@ -140,9 +140,18 @@ def _under(stream, call, *args, **kw):
     """`stream=` of a call: the call as made under torch.cuda.stream(stream), so
     that the allocator hands out, and takes back, on that stream what the call
     writes there. (A block of the current stream's pool may still be in use by
-    that stream's pending kernels, a call's scratch above all.)"""
+    that stream's pending kernels, a call's scratch above all.) The outputs are
+    recorded for the caller's stream too: one that is read there, and dropped, is
+    not handed out again before that read."""
+    caller = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
-        return call(*args, **kw)
+        out = call(*args, **kw)
+    if caller != stream:
+        outs = (out,) if torch.is_tensor(out) else out if type(out) is tuple else vars(out).values()
+        for t in outs:
+            if torch.is_tensor(t):
+                t.record_stream(caller)
+    return out
 
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}

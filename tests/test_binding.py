@@ -73,7 +73,11 @@ def fake(moe, monkeypatch):
         yield
         f.inside = before
 
+    f.recorded = []
+    f.caller = types.SimpleNamespace(cuda_stream=0xCA11)
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: f.caller)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: f.recorded.append((id(t), s)))
     monkeypatch.setattr(moe, "lib", f)
     monkeypatch.setattr(moe, "_dev", lambda *ts: None)
     monkeypatch.setattr(moe, "_on", lambda *ts: f.inside)
@@ -124,12 +128,17 @@ def test_a_call_on_another_stream_allocates_there(moe, fake, monkeypatch, name):
     monkeypatch.setattr(torch, "empty", noting(torch.empty))
     monkeypatch.setattr(torch, "empty_like", noting(torch.empty_like))
     monkeypatch.setattr(moe, "_empty", noting(moe._empty))
-    side = types.SimpleNamespace(cuda_stream=0x51DE)
-    getattr(moe, name)(*args, stream=side)
+    side = types.SimpleNamespace(cuda_stream=0x51DE, device=0)
+    out = getattr(moe, name)(*args, stream=side)
     assert made and all(m is side for m in made)
     launches = [a for n, a in fake.calls if n == "moe_" + name]
     assert len(launches) == 1 and launches[0][-1] is side
     assert fake.inside is None
+    # outputs go back to that stream's pool only after the caller's reads
+    outs = [out] if torch.is_tensor(out) else out if isinstance(out, tuple) else vars(out).values()
+    outs = [t for t in outs if torch.is_tensor(t)]
+    assert outs and sorted(fake.recorded, key=str) == \
+        sorted([(id(t), fake.caller) for t in outs], key=str)
 
 
 @gpu
