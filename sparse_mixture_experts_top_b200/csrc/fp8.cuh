@@ -40,9 +40,10 @@ __device__ __forceinline__ float code_arg(float v, float r) {
 // g = -3, 1.5e-3 at -4 and half at -5, and zero from -5.5 down. A 16-bit h hides
 // that below its own last place; a block of codes does not, whose scale follows
 // its largest magnitude down to 2^-100. (It is also the shorter one: gate|up of
-// 20,480 rows over 512 experts 210 against 222 us on one B200.) The error relative to the result is below
-// (8 + 3.2 |2z|) 2^-23: the argument's roundings (4 |2z| of 2^-24) and the fast
-// exponential's 2 + 1.16 |2z|. Past 2z = -87 (g below -9.4) the result is zero.
+// 20,480 rows over 512 experts 210 against 222 us on one B200.) The error relative
+// to the result is below (8 + 3.2 |2z|) 2^-23: the argument's roundings (4 |2z| of
+// 2^-24) and the fast exponential's 2 + 1.16 |2z|. Past 2z = -87 (g below -9.4) the
+// result is zero.
 __device__ __forceinline__ float glu_codes(int act, float g, float u) {
   if (act == MOE_ACT_GEGLU_TANH) {
     const float m2z = -1.5957691216057308f * fmaf(0.044715f * g, g * g, g);
